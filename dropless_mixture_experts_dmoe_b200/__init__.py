@@ -3,7 +3,10 @@ tcgen05 gated-SiLU expert GEMMs, weighted combine and backward, behind the C ABI
 ``libdmoe.so`` (include/dmoe.h).  ``binding`` is the thin ctypes layer over it."""
 from . import autograd, binding  # noqa: F401
 from .autograd import DMoEFunction, dmoe  # noqa: F401
-from .binding import (Buffers, DMoEError, SparseMap, dmoe_backward, dmoe_bwd_dglu,  # noqa: F401
+from .binding import (Buffers, DMoEError, FewBuffers, Mx4, Mx4Buffers, SparseMap,  # noqa: F401
+                      dmoe_forward_few, dmoe_mx4_dequantize, dmoe_mx4_forward,
+                      dmoe_mx4_forward_few, dmoe_mx4_quantize)
+from .binding import (dmoe_backward, dmoe_bwd_dglu,  # noqa: F401
                       dmoe_bwd_dx, dmoe_bwd_scatter, dmoe_bwd_wgrad, dmoe_expert_down,
                       dmoe_expert_glu, dmoe_expert_glu_gather, dmoe_forward, dmoe_padded_gather, dmoe_padded_rows_max,
                       dmoe_padded_scatter, dmoe_router_backward, dmoe_router_dlogits,

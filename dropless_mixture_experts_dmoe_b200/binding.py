@@ -20,7 +20,10 @@ BLOCKING = 128
 MAX_EXPERTS = 1024
 MAX_TOP_K = 32
 
+FEW_MAX_TOKENS = 128
+
 WS_MAP, WS_FORWARD, WS_BACKWARD, WS_FORWARD_TRAIN, WS_ROUTER_BACKWARD = 0, 1, 2, 3, 4
+WS_FEW, WS_MX4_FORWARD = 6, 7
 DGLU_TILE_COLS = 128
 
 STATUS_NONFINITE_LOGITS = 0x1
@@ -62,6 +65,10 @@ MAP_FIELDS = ("top_experts", "weights", "tokens_per_expert", "bins", "padded_bin
 
 class dmoe_map(ctypes.Structure):
     _fields_ = [(n, _P) for n in MAP_FIELDS]
+
+
+class dmoe_mx4(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P)]
 
 
 class DMoEError(RuntimeError):
@@ -109,12 +116,21 @@ def load():
     lib.dmoe_bwd_dx.argtypes = [D, _P, _P, _P, _P, M, _P, _P, _P]
     lib.dmoe_bwd_wgrad.argtypes = [D, _P, _P, _P, _P, _P, M, _P, _P, _P, _P]
     lib.dmoe_sparse_map_noalloc.argtypes = [D, _P, M, _P]
+    Q = ctypes.POINTER(dmoe_mx4)
+    i64 = ctypes.c_int64
+    lib.dmoe_forward_few.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.dmoe_mx4_forward_few.argtypes = [D, _P, _P, Q, Q, Q, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.dmoe_mx4_quantize.argtypes = [i64, i64, _P, Q, _P]
+    lib.dmoe_mx4_dequantize.argtypes = [i64, i64, Q, _P, _P]
+    lib.dmoe_mx4_forward.argtypes = [D, _P, Q, Q, Q, M, _P, _P, _SZ, _P]
     for fn in ("dmoe_sparse_map", "dmoe_sparse_map_noalloc", "dmoe_forward", "dmoe_backward",
                "dmoe_padded_gather",
                "dmoe_expert_glu", "dmoe_expert_glu_gather", "dmoe_expert_down", "dmoe_padded_scatter",
                "dmoe_expert_down_combine",
                "dmoe_bwd_dglu", "dmoe_bwd_dx", "dmoe_bwd_wgrad", "dmoe_bwd_scatter",
-               "dmoe_router_forward", "dmoe_router_dlogits", "dmoe_router_backward"):
+               "dmoe_router_forward", "dmoe_router_dlogits", "dmoe_router_backward",
+               "dmoe_forward_few", "dmoe_mx4_forward_few", "dmoe_mx4_quantize",
+               "dmoe_mx4_dequantize", "dmoe_mx4_forward"):
         getattr(lib, fn).restype = _I
     lib.dmoe_error_string.argtypes = [_I]
     lib.dmoe_error_string.restype = ctypes.c_char_p
@@ -357,6 +373,126 @@ def dmoe_sparse_map_noalloc(dims: dmoe_dims, logits, smap: SparseMap, stream=Non
     _check(load().dmoe_sparse_map_noalloc(ctypes.byref(dims), _ptr(logits),
                                           ctypes.byref(smap.c), _stream(stream)),
            "dmoe_sparse_map_noalloc")
+
+
+# ---- serving: the layer for a few tokens, and the microscaled 4-bit format ------------------------
+
+class Mx4:
+    """A matrix, or a stack of expert matrices, in the microscaled 4-bit format (see dmoe_mx4 in
+    include/dmoe.h): ``codes`` [..., rows, cols / 2] and ``scales`` [..., ceil(rows/128), cols/128,
+    32, 4, 4], contiguous uint8 tensors.  In a stack ``rows`` is a multiple of 128."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not (
+                codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous uint8 tensors")
+        self.shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+        if codes.dim() < 2 or tuple(scales.shape) != self.scales_shape(*self.shape):
+            raise ValueError(f"scales of codes {tuple(codes.shape)}: {tuple(scales.shape)}")
+        self.codes, self.scales = codes, scales
+        self._c = dmoe_mx4(codes.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def scales_shape(*shape) -> tuple:
+        """Shape of the scale tensor of a [..., rows, cols] matrix."""
+        *lead, rows, cols = shape
+        if rows < 1 or cols < 128 or cols % 128 or (lead and rows % 128):
+            raise ValueError("cols, and the rows of a stack, must be multiples of 128")
+        return (*lead, (rows + 127) // 128, cols // 128, 32, 4, 4)
+
+    @classmethod
+    def empty(cls, *shape, device="cuda") -> "Mx4":
+        scales = cls.scales_shape(*shape)
+        return cls(torch.empty((*shape[:-1], shape[-1] // 2), dtype=torch.uint8, device=device),
+                   torch.empty(scales, dtype=torch.uint8, device=device))
+
+
+def _rows_cols(shape):
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return rows, shape[-1]
+
+
+def dmoe_mx4_quantize(src, dst: Mx4, stream=None):
+    """dst = src (bf16, the shape of dst) in the microscaled 4-bit format."""
+    rows, cols = _rows_cols(dst.shape)
+    _check(load().dmoe_mx4_quantize(rows, cols, _ptr(src), dst.ref, _stream(stream)),
+           "dmoe_mx4_quantize")
+
+
+def dmoe_mx4_dequantize(src: Mx4, dst, stream=None):
+    """dst (bf16) = the values of src."""
+    rows, cols = _rows_cols(src.shape)
+    _check(load().dmoe_mx4_dequantize(rows, cols, src.ref, _ptr(dst), _stream(stream)),
+           "dmoe_mx4_dequantize")
+
+
+class FewBuffers:
+    """Device buffers of the few-token calls for one shape: ``top_experts`` [T,k] and ``weights``
+    [T,k] (outputs when logits are given, else inputs), ``status`` (starts at 0, bits are OR-ed
+    in) and the workspace ``ws``."""
+
+    def __init__(self, dims: dmoe_dims, device="cuda"):
+        n = dmoe_workspace_bytes(dims, WS_FEW)
+        if n == 0:
+            raise DMoEError(-2, "FewBuffers")
+        self.dims = dims
+        self.top_experts = torch.empty((dims.T, dims.top_k), dtype=torch.int32, device=device)
+        self.weights = torch.empty((dims.T, dims.top_k), dtype=torch.float32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+        self._args = (self.top_experts.data_ptr(), self.weights.data_ptr(),
+                      self.status.data_ptr(), self.ws.data_ptr(), n)
+
+
+def dmoe_forward_few(dims: dmoe_dims, x, logits, w1, w3, w2, bufs: FewBuffers, y, stream=None):
+    """The whole layer for T <= FEW_MAX_TOKENS tokens, from the logits [T,E] to y [T,h].  logits
+    None: bufs.top_experts and bufs.weights are taken as given."""
+    top, weights, status, ws, n = bufs._args
+    _check(load().dmoe_forward_few(ctypes.byref(dims), _ptr(x), _ptr(logits), _ptr(w1), _ptr(w3),
+                                   _ptr(w2), top, weights, _ptr(y), status, ws, n,
+                                   _stream(stream)), "dmoe_forward_few")
+
+
+def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, bufs: FewBuffers,
+                         y, stream=None):
+    """dmoe_forward_few over expert weights in the microscaled 4-bit format."""
+    top, weights, status, ws, n = bufs._args
+    _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), _ptr(x), _ptr(logits), w1.ref, w3.ref,
+                                       w2.ref, top, weights, _ptr(y), status, ws, n,
+                                       _stream(stream)), "dmoe_mx4_forward_few")
+
+
+class Mx4Buffers:
+    """Device buffers of the 4-bit layer over many tokens for one shape: the sparse map and its
+    workspace, and the forward's workspace ``ws``.  After a forward ``hidden()`` is a view of the
+    workspace: H of the padded rows in the 4-bit format."""
+
+    def __init__(self, dims: dmoe_dims, device="cuda"):
+        self.dims = dims
+        self.map = SparseMap(dims, device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.ws_map = torch.empty(max(dmoe_workspace_bytes(dims, WS_MAP), 16), **u8)
+        self.ws = torch.empty(dmoe_workspace_bytes(dims, WS_MX4_FORWARD), **u8)
+
+    def hidden(self) -> Mx4:
+        P, h, f = dmoe_padded_rows_max(self.dims), self.dims.hidden, self.dims.ffn
+        up = lambda v: (v + 255) // 256 * 256
+        o_q = up(up(P * h // 2) + P * h // 32)
+        o_s = up(o_q + P * f // 2)
+        return Mx4(self.ws[o_q:o_q + P * f // 2].view(P, f // 2),
+                   self.ws[o_s:o_s + P * f // 32].view(Mx4.scales_shape(P, f)))
+
+
+def dmoe_mx4_forward(dims: dmoe_dims, x, w1: Mx4, w3: Mx4, w2: Mx4, smap: SparseMap, y, ws,
+                     stream=None):
+    """y [T,h] = the layer with every product in the microscaled 4-bit format (inference)."""
+    _check(load().dmoe_mx4_forward(ctypes.byref(dims), _ptr(x), w1.ref, w3.ref, w2.ref,
+                                   ctypes.byref(smap.c), _ptr(y), _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)),
+           "dmoe_mx4_forward")
 
 
 # ---- buffers (allocation only) ----------------------------------------------------------------

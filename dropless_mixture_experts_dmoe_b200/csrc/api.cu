@@ -230,6 +230,84 @@ void saved_layout(const dmoe_dims *d, size_t off[3], size_t *total) {
   *total = align_up(off[2] + P * d->ffn * 2);
 }
 
+// Few-token workspace: H [T*k, f] fp32.
+inline size_t few_bytes(const dmoe_dims *d) {
+  return align_up((size_t)d->T * d->top_k * d->ffn * sizeof(float));
+}
+
+inline int check_few_dims(const dmoe_dims *d) {
+  int rc = check_dims(d);
+  if (rc) return rc;
+  return (d->T <= DMOE_FEW_MAX_TOKENS && !rounding(d)) ? DMOE_OK : DMOE_ERR_SHAPE;
+}
+
+inline int check_mx4(const dmoe_mx4 *m) {
+  if (!m || !m->codes || !m->scales) return DMOE_ERR_NULL;
+  return (aligned16(m->codes) && aligned16(m->scales)) ? DMOE_OK : DMOE_ERR_ALIGN;
+}
+
+// The first NULL, then the first misaligned one of three matrices.
+inline int check_mx4(const dmoe_mx4 *a, const dmoe_mx4 *b, const dmoe_mx4 *c) {
+  const int ra = check_mx4(a), rb = check_mx4(b), rc = check_mx4(c);
+  if (ra == DMOE_ERR_NULL || rb == DMOE_ERR_NULL || rc == DMOE_ERR_NULL) return DMOE_ERR_NULL;
+  return ra ? ra : rb ? rb : rc;
+}
+
+int forward_few(const dmoe_dims *dims, const void *x, const void *logits, FewWeights w1,
+                FewWeights w3, FewWeights w2, int32_t *top, float *weights, void *y,
+                int32_t *status, void *ws, size_t ws_bytes, void *stream) {
+  if (!x || !top || !weights || !y || !status || !ws) return DMOE_ERR_NULL;
+  if (ws_bytes < few_bytes(dims)) return DMOE_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(logits) || !aligned16(top) || !aligned16(weights) ||
+      !aligned16(y) || !aligned16(ws))
+    return DMOE_ERR_ALIGN;
+  int rc = check_device();
+  if (rc) return rc;
+  FewParams p;
+  p.T = dims->T;
+  p.k = dims->top_k;
+  p.E = dims->num_experts;
+  p.h = dims->hidden;
+  p.f = dims->ffn;
+  p.x = x;
+  p.w1 = w1;
+  p.w3 = w3;
+  p.w2 = w2;
+  p.top = top;
+  p.weights = weights;
+  p.hbuf = static_cast<float *>(ws);
+  p.y = static_cast<__nv_bfloat16 *>(y);
+  return launch_rc(launch_few(p, static_cast<const uint16_t *>(logits),
+                              (dims->flags & DMOE_ROUTE_RENORMALIZE) != 0, top, weights, status,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+// 4-bit forward workspace: X_pad codes [P, h/2] | its scales [P*h/32] | H codes [P, f/2] | its
+// scales [P*f/32] | Y_pad [P,h] fp16 | Y_pad scales [P, dmoe_scale_stride(h)] fp32
+struct Mx4Layout {
+  size_t xq, xs, hq, hs, ypad, yscale, total;
+};
+Mx4Layout mx4_layout(const dmoe_dims *d) {
+  const size_t P = (size_t)pmax_of(d);
+  Mx4Layout l;
+  l.xq = 0;
+  l.xs = align_up(l.xq + P * d->hidden / 2);
+  l.hq = align_up(l.xs + P * d->hidden / 32);
+  l.hs = align_up(l.hq + P * d->ffn / 2);
+  l.ypad = align_up(l.hs + P * d->ffn / 32);
+  l.yscale = align_up(l.ypad + P * d->hidden * 2);
+  l.total = align_up(l.yscale + P * scale_cols(d) * sizeof(float));
+  return l;
+}
+
+int check_mx4_matrix(int64_t rows, int64_t cols) {
+  if (rows < 1 || cols < DMOE_BLOCKING || cols % DMOE_BLOCKING != 0) return DMOE_ERR_SHAPE;
+  // element offsets stay within 64 bits, column tiles within 32
+  return (rows <= (1LL << 40) && cols <= (1LL << 30) && rows <= (1LL << 60) / cols)
+             ? DMOE_OK
+             : DMOE_ERR_TOO_LARGE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -257,6 +335,10 @@ size_t dmoe_workspace_bytes(const dmoe_dims *dims, int kind) {
       return router_layout(dims).total;
     case DMOE_WS_BACKWARD:
       return bwd_layout(dims).total;
+    case DMOE_WS_FEW:
+      return check_few_dims(dims) == DMOE_OK ? few_bytes(dims) : 0;
+    case DMOE_WS_MX4_FORWARD:
+      return mx4_layout(dims).total;
     default:
       return 0;
   }
@@ -610,6 +692,109 @@ int dmoe_router_backward(const dmoe_dims *dims, const void *x, const void *w_rou
   if ((rc = launch_rc(launch_router_wgrad_gemm(T, h, E, dl, x, part, splits, map->status, st))))
     return rc;
   return launch_rc(launch_router_wgrad_reduce(h, E, splits, part, dw_router, st));
+}
+
+int dmoe_forward_few(const dmoe_dims *dims, const void *x, const void *logits, const void *w1,
+                     const void *w3, const void *w2, int32_t *top_experts, float *weights, void *y,
+                     int32_t *status, void *ws, size_t ws_bytes, void *stream) {
+  int rc = check_few_dims(dims);
+  if (rc) return rc;
+  if (!w1 || !w3 || !w2) return DMOE_ERR_NULL;
+  if (!aligned16(w1) || !aligned16(w3) || !aligned16(w2)) return DMOE_ERR_ALIGN;
+  return forward_few(dims, x, logits, FewWeights{w1, nullptr}, FewWeights{w3, nullptr},
+                     FewWeights{w2, nullptr}, top_experts, weights, y, status, ws, ws_bytes,
+                     stream);
+}
+
+int dmoe_mx4_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
+                         const dmoe_mx4 *w1, const dmoe_mx4 *w3, const dmoe_mx4 *w2,
+                         int32_t *top_experts, float *weights, void *y, int32_t *status, void *ws,
+                         size_t ws_bytes, void *stream) {
+  int rc = check_few_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_mx4(w1, w3, w2))) return rc;
+  return forward_few(dims, x, logits, FewWeights{w1->codes, w1->scales},
+                     FewWeights{w3->codes, w3->scales}, FewWeights{w2->codes, w2->scales},
+                     top_experts, weights, y, status, ws, ws_bytes, stream);
+}
+
+int dmoe_mx4_quantize(int64_t rows, int64_t cols, const void *src, const dmoe_mx4 *dst,
+                      void *stream) {
+  int rc = check_mx4_matrix(rows, cols);
+  if (rc) return rc;
+  if (!src) return DMOE_ERR_NULL;
+  if ((rc = check_mx4(dst))) return rc;
+  if (!aligned16(src)) return DMOE_ERR_ALIGN;
+  if ((rc = check_device())) return rc;
+  return launch_rc(launch_mx4_quantize(rows, cols, src, dst->codes, dst->scales,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src, void *dst,
+                        void *stream) {
+  int rc = check_mx4_matrix(rows, cols);
+  if (rc) return rc;
+  if (!dst) return DMOE_ERR_NULL;
+  if ((rc = check_mx4(src))) return rc;
+  if (!aligned16(dst)) return DMOE_ERR_ALIGN;
+  if ((rc = check_device())) return rc;
+  return launch_rc(launch_mx4_dequantize(rows, cols, src->codes, src->scales, dst,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1, const dmoe_mx4 *w3,
+                     const dmoe_mx4 *w2, const dmoe_map *map, void *y, void *ws, size_t ws_bytes,
+                     void *stream) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_map(map, true, dims))) return rc;
+  if (!x || !y || !ws) return DMOE_ERR_NULL;
+  rc = check_mx4(w1, w3, w2);
+  if (rc == DMOE_ERR_NULL) return rc;
+  const Mx4Layout l = mx4_layout(dims);
+  if (ws_bytes < l.total) return DMOE_ERR_WORKSPACE;
+  if (rc) return rc;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return DMOE_ERR_ALIGN;
+  if ((rc = check_device())) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  float *yscale = reinterpret_cast<float *>(w + l.yscale);
+  const long long max_blocks = pmax_of(dims) / DMOE_BLOCKING;
+  if ((rc = launch_rc(launch_mx4_gather(dims->T, dims->hidden, dims->top_k, dims->num_experts, x,
+                                        map->dest_row, map->tokens_per_expert, map->padded_bins,
+                                        w + l.xq, w + l.xs, st, entry_offsets_of(dims, map)))))
+    return rc;
+  Mx4GemmParams p;
+  p.E = dims->num_experts;
+  p.h = dims->hidden;
+  p.f = dims->ffn;
+  p.num_blocks = map->num_blocks;
+  p.block_expert = map->block_expert;
+  p.padded_bins = map->padded_bins;
+  p.bins = map->bins;
+  p.indices = map->indices;
+  p.weights = map->weights;
+  p.status = map->status;
+  p.a = w + l.xq;
+  p.as = w + l.xs;
+  p.w1 = static_cast<const uint8_t *>(w1->codes);
+  p.w1s = static_cast<const uint8_t *>(w1->scales);
+  p.w3 = static_cast<const uint8_t *>(w3->codes);
+  p.w3s = static_cast<const uint8_t *>(w3->scales);
+  p.out = w + l.hq;
+  p.outs = w + l.hs;
+  p.yscale = nullptr;
+  if ((rc = launch_rc(launch_mx4_glu(p, max_blocks, st)))) return rc;
+  p.a = w + l.hq;
+  p.as = w + l.hs;
+  p.w1 = static_cast<const uint8_t *>(w2->codes);
+  p.w1s = static_cast<const uint8_t *>(w2->scales);
+  p.w3 = p.w3s = nullptr;
+  p.out = w + l.ypad;
+  p.outs = nullptr;
+  p.yscale = yscale;
+  if ((rc = launch_rc(launch_mx4_down(p, max_blocks, st)))) return rc;
+  return dmoe_padded_scatter(dims, w + l.ypad, yscale, map, nullptr, y, stream);  // rows weighted
 }
 
 const char *dmoe_error_string(int code) {

@@ -1,6 +1,7 @@
 // kernels.h -- host-side launchers of the dMoE kernels (internal to libdmoe.so).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -157,6 +158,47 @@ cudaError_t launch_router_wgrad_reduce(int h, int E, int splits, const float *pa
 cudaError_t launch_router_dlogits(int T, int E, int k, bool renorm, const uint16_t *logits,
                                   const int32_t *top, const float *dweights, uint16_t *dlogits,
                                   cudaStream_t st);
+
+// The layer for a few tokens (few.cu): expert weights in bf16 (scales NULL) or in the
+// microscaled 4-bit format.
+struct FewWeights {
+  const void *data, *scales;
+};
+struct FewParams {
+  int T, k, E, h, f;
+  const void *x;  // [T, h] bf16
+  FewWeights w1, w3, w2;
+  const int32_t *top;    // [T, k]
+  const float *weights;  // [T, k]
+  float *hbuf;           // [T*k, f]
+  __nv_bfloat16 *y;      // [T, h]
+};
+// logits given: top and weights are written first; else they are inputs.
+cudaError_t launch_few(const FewParams &p, const uint16_t *logits, bool renorm, int32_t *top,
+                       float *weights, int32_t *status, cudaStream_t st);
+
+// The microscaled 4-bit format (mx4.cu, mx4_gemm.cu).
+cudaError_t launch_mx4_quantize(long long rows, long long cols, const void *src, void *codes,
+                                void *scales, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(long long rows, long long cols, const void *codes,
+                                  const void *scales, void *dst, cudaStream_t st);
+cudaError_t launch_mx4_gather(int T, int h, int k, int E, const void *x, const int32_t *dest_row,
+                              const int32_t *counts, const int32_t *padded_bins, void *codes,
+                              void *scales, cudaStream_t st, const int32_t *offsets);
+struct Mx4GemmParams {
+  int E, h, f;
+  const int32_t *num_blocks, *block_expert, *padded_bins, *bins, *indices;
+  const float *weights;
+  const uint8_t *a, *as;    // left operand [P_max, K] in the format
+  const uint8_t *w1, *w1s;  // W1 (GLU) or W2 (DOWN)
+  const uint8_t *w3, *w3s;  // W3 (GLU)
+  uint8_t *out;             // GLU: H elements [P_max, f / 2]; DOWN: Y_pad [P_max, h] fp16
+  uint8_t *outs;            // GLU: scales of H
+  float *yscale;            // DOWN: scales of Y_pad's rows
+  int32_t *status;
+};
+cudaError_t launch_mx4_glu(const Mx4GemmParams &p, long long max_blocks, cudaStream_t st);
+cudaError_t launch_mx4_down(const Mx4GemmParams &p, long long max_blocks, cudaStream_t st);
 
 int device_sm_count();
 

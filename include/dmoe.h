@@ -196,6 +196,8 @@ typedef struct {
 #define DMOE_WS_BACKWARD 2       /* dmoe_backward */
 #define DMOE_WS_FORWARD_TRAIN 3  /* dmoe_forward with saved != NULL (training) */
 #define DMOE_WS_ROUTER_BACKWARD 4 /* dmoe_router_backward */
+#define DMOE_WS_FEW 6             /* dmoe_forward_few, dmoe_mx4_forward_few (5 is unassigned) */
+#define DMOE_WS_MX4_FORWARD 7     /* dmoe_mx4_forward */
 
 /* Columns per routing-weight partial sum of the dH GEMM: dmoe_bwd_dglu's partials have
  * ceil(ffn / DMOE_DGLU_TILE_COLS) columns per row. */
@@ -429,6 +431,77 @@ DMOE_API int dmoe_router_backward(const dmoe_dims *dims, const void *x, const vo
                                   const void *logits, const dmoe_map *map, const float *dweights,
                                   void *dx, float *dw_router, void *ws, size_t ws_bytes,
                                   void *stream);
+
+/* ---- Serving: the layer for a few tokens. ---- */
+
+/* Tokens that the few-token calls take at most (a decode batch; one padded row block). */
+#define DMOE_FEW_MAX_TOKENS 128
+
+/* The whole layer for T <= DMOE_FEW_MAX_TOKENS tokens, from the logits to y, with no padding, no
+ * sparse map and no copies of x: reading the weights of the experts in use is what bounds it.
+ *   x [T,h], w1, w3 [E,f,h], w2 [E,h,f] bf16 as in dmoe_forward;
+ *   logits: [T,E] bf16, or NULL to take top_experts and weights [T,k] as given;
+ *   top_experts [T,k] int32, weights [T,k] fp32: the routing (dmoe_map has their meaning).
+ *     Outputs when logits are given; the experts are those of dmoe_sparse_map, the weights
+ *     agree with its to fp32 rounding.  Given experts outside [0, E) set
+ *     DMOE_STATUS_EXPERT_OUT_OF_RANGE and add nothing; an expert given twice for a token counts
+ *     twice and sets DMOE_STATUS_DUPLICATE_EXPERT;
+ *   y [T,h] bf16 = sum_s w_ts * (H_ts W2_e^T), fp32 sums, rounded once;
+ *   status: the call's bits are OR-ed into this int32 word;
+ *   ws: dmoe_workspace_bytes(dims, DMOE_WS_FEW) bytes.
+ * Needs no map.  DMOE_ROUTE_RENORMALIZE is followed; DMOE_SAVE_X_ONLY and DMOE_FUSED_COMBINE
+ * choose between forms of dmoe_forward and change nothing here; DMOE_ROUTE_TOKEN_ROUNDING and
+ * T > DMOE_FEW_MAX_TOKENS are DMOE_ERR_SHAPE.  Results are deterministic. */
+DMOE_API int dmoe_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
+                              const void *w1, const void *w3, const void *w2,
+                              int32_t *top_experts, float *weights, void *y, int32_t *status,
+                              void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Serving: the microscaled 4-bit format. ---- */
+
+/* A matrix [rows, cols] in the microscaled 4-bit format (cols a multiple of 128): blocks of 32
+ * consecutive columns share one power-of-two scale.
+ *   codes  [rows, cols / 2] bytes: column 2i in the low, 2i + 1 in the high four bits of byte i;
+ *          an element is sign, two exponent bits, one mantissa bit (e2m1): 0, 0.5, 1, 1.5, 2, 3,
+ *          4, 6 and their negatives;
+ *   scales [ceil(rows/128), cols/128, 32, 4, 4] bytes: byte [i][j][l][q][b] is the scale of row
+ *          128 i + 32 q + l, columns 128 j + 32 b .. + 31, as an exponent s (e8m0): 2^(s - 127);
+ *          255 is NaN.
+ * A stack of expert matrices [E, n, cols] (n a multiple of 128) is the matrix [E * n, cols].
+ * Both pointers 16-byte aligned. */
+typedef struct {
+  void *codes;
+  void *scales;
+} dmoe_mx4;
+
+/* src [rows, cols] bf16 -> dst.  Per block, with m the largest magnitude,
+ * s = floor(log2 m) - 2 + 127 kept within [0, 254] (0 for an all-zero block) and every element
+ * the nearest e2m1 value to x / 2^(s - 127), ties to the even mantissa, saturated at +-6.  A
+ * block that holds an inf or NaN gets the scale NaN and zero codes.  Scale bytes of the rows
+ * that fill the last tile are written as 0. rows >= 1. */
+DMOE_API int dmoe_mx4_quantize(int64_t rows, int64_t cols, const void *src, const dmoe_mx4 *dst,
+                               void *stream);
+/* src -> dst [rows, cols] bf16: element times scale.  Exact, except that a product beyond bf16's
+ * largest value (scale bytes 252 and above) is an inf. */
+DMOE_API int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src, void *dst,
+                                 void *stream);
+
+/* dmoe_forward_few over expert weights in the format (w1, w3 as [E * f, h], w2 as [E * h, f]);
+ * x and the sums keep their precision, only the weights have four bits. */
+DMOE_API int dmoe_mx4_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
+                                  const dmoe_mx4 *w1, const dmoe_mx4 *w3, const dmoe_mx4 *w2,
+                                  int32_t *top_experts, float *weights, void *y,
+                                  int32_t *status, void *ws, size_t ws_bytes, void *stream);
+
+/* The layer for many tokens with both operands of every product in the format (inference):
+ * token rows of x are converted as dmoe_mx4_quantize does, H = silu(A) * Bm is converted from
+ * fp32 in the same way, and the products run on the block-scaled tensor cores with fp32
+ * accumulation.  map: from dmoe_sparse_map.  y [T,h] bf16, the weighted sum of a token's rows.
+ * ws: dmoe_workspace_bytes(dims, DMOE_WS_MX4_FORWARD) bytes.  DMOE_SAVE_X_ONLY and
+ * DMOE_FUSED_COMBINE change nothing here; both routing flags are followed through the map. */
+DMOE_API int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1,
+                              const dmoe_mx4 *w3, const dmoe_mx4 *w2, const dmoe_map *map, void *y,
+                              void *ws, size_t ws_bytes, void *stream);
 
 /* ---- Diagnostics. ---- */
 DMOE_API const char *dmoe_error_string(int code);

@@ -1,0 +1,284 @@
+"""The layer for a few tokens against 64-bit references: sizes, routings given and computed,
+empty and non-finite rows, refusals' counterparts on the device, streams and graphs, over bf16
+and microscaled 4-bit expert weights."""
+import pytest
+import torch
+
+from dropless_mixture_experts_dmoe_b200 import binding as B
+
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+# (T, h, f, E, k)
+SHAPES = [
+    (1, 128, 128, 1, 1),       # the smallest call
+    (1, 1536, 256, 128, 8),    # one token of the high-granularity workload
+    (2, 128, 1664, 3, 3),      # every expert chosen, f an odd number of 128s
+    (3, 1408, 384, 5, 2),
+    (7, 640, 128, 33, 4),
+    (8, 2048, 512, 256, 8),
+    (9, 256, 896, 16, 1),
+    (17, 2048, 1024, 64, 8),
+    (31, 128, 128, 1000, 32),  # more entries than rows of anything else
+    (33, 4096, 256, 8, 8),     # more than 32 tokens at every expert
+    (64, 384, 2048, 4, 2),
+    (100, 1152, 128, 2, 1),
+    (128, 512, 640, 128, 6),
+    (128, 256, 384, 2, 2),     # 128 tokens at both experts
+]
+IDS = ["-".join(map(str, s)) for s in SHAPES]
+
+
+def make(shape, seed=0, mx4=False, wscale=0.05):
+    T, h, f, E, k = shape
+    g = torch.Generator(device="cuda").manual_seed(100 + seed)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    d = dict(x=n(T, h).bfloat16(), logits=n(T, E).bfloat16(), w1=(wscale * n(E, f, h)).bfloat16(),
+             w3=(wscale * n(E, f, h)).bfloat16(), w2=(wscale * n(E, h, f)).bfloat16())
+    d["dims"] = B.make_dims(T, h, f, E, k)
+    for w in ("w1", "w3", "w2"):
+        if mx4:
+            q = B.Mx4.empty(*d[w].shape)
+            B.dmoe_mx4_quantize(d[w], q)
+            torch.cuda.synchronize()
+            d[w + "_64"] = R.mx4_decode_values(q.codes, q.scales)
+            d[w] = q
+        else:
+            d[w + "_64"] = d[w].double()
+    d["mx4"] = mx4
+    return d
+
+
+def run(d, bufs, y, logits="logits", stream=None):
+    call = B.dmoe_mx4_forward_few if d["mx4"] else B.dmoe_forward_few
+    call(d["dims"], d["x"], d[logits] if logits else None, d["w1"], d["w3"], d["w2"], bufs, y,
+         stream=stream)
+
+
+def outputs(d):
+    """Buffers with every output and the workspace poisoned; y with a guard row behind it."""
+    bufs = B.FewBuffers(d["dims"])
+    bufs.ws.fill_(255)
+    bufs.top_experts.fill_(-7)
+    bufs.weights.fill_(float("nan"))
+    yg = torch.full((d["dims"].T + 1, d["dims"].hidden), 7.0, dtype=torch.bfloat16, device="cuda")
+    yg[:-1] = float("nan")
+    return bufs, yg
+
+
+def reference(d, top, wts):
+    return R.layer(d["x"].double(), d["w1_64"], d["w3_64"], d["w2_64"], top, wts,
+                   h_rel=2.0 ** -11 if d["mx4"] else 2.0 ** -16)
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_few_parity(shape, mx4):
+    d = make(shape, mx4=mx4)
+    bufs, yg = outputs(d)
+    run(d, bufs, yg[:-1])
+    torch.cuda.synchronize()
+    top, wts = R.route(d["logits"], shape[4])
+    assert int(bufs.status.item()) == 0
+    assert torch.equal(bufs.top_experts.long(), top)
+    # fp32 expf and sums of E terms: a few steps of 2^-24
+    assert ((bufs.weights.double() - wts).abs() <= (8 + shape[3] ** 0.5) * 2.0 ** -24 * wts).all()
+    y, tol = reference(d, top, wts)
+    R.check(yg[:-1], y, tol, "y")
+    assert (yg[-1] == 7.0).all()
+    # again, in other poisoned buffers: bit for bit
+    bufs2, yg2 = outputs(d)
+    run(d, bufs2, yg2[:-1])
+    assert same(yg, yg2) and torch.equal(bufs.weights, bufs2.weights)
+
+
+@pytest.mark.parametrize("shape", [SHAPES[4], SHAPES[7], SHAPES[8]])
+def test_few_routes_as_the_map_does(shape):
+    """The same experts as dmoe_sparse_map; weights to fp32 rounding, renormalised too."""
+    T, h, f, E, k = shape
+    d = make(shape, seed=3)
+    d["logits"][0] = 0.25  # all equal: the first k experts
+    d["logits"][1, ::2] = -0.0
+    for flags in (0, B.ROUTE_RENORMALIZE, B.SAVE_X_ONLY | B.FUSED_COMBINE):
+        dims = d["dims"] = B.make_dims(T, h, f, E, k, flags=flags)
+        bufs, yg = outputs(d)
+        run(d, bufs, yg[:-1])
+        full = B.Buffers(dims)
+        B.dmoe_sparse_map(dims, d["logits"], full.map, full.ws_map)
+        torch.cuda.synchronize()
+        assert torch.equal(bufs.top_experts, full.map.top_experts)
+        assert torch.allclose(bufs.weights, full.map.weights, rtol=2e-6, atol=0)
+        _, wts = R.route(d["logits"], k, bool(flags & B.ROUTE_RENORMALIZE))
+        y, tol = reference(d, bufs.top_experts.long(), wts)
+        R.check(yg[:-1], y, tol, "y")
+
+
+def test_few_agrees_with_the_full_layer():
+    """The decode step and the prompt path of one layer: dmoe_forward rounds H to bf16 (half a
+    step 2^-8 of each term), so the two differ by at most that on top of both bounds."""
+    d = make((24, 512, 384, 16, 4), seed=5)
+    dims = d["dims"]
+    bufs, yg = outputs(d)
+    run(d, bufs, yg[:-1])
+    full = B.Buffers(dims)
+    y2 = torch.empty_like(d["x"])
+    B.dmoe_sparse_map(dims, d["logits"], full.map, full.ws_map)
+    B.dmoe_forward(dims, d["x"], d["w1"], d["w3"], d["w2"], full.map, y2, ws=full.ws_fwd)
+    top, wts = R.route(d["logits"], dims.top_k)
+    y, tol = R.layer(d["x"].double(), d["w1_64"], d["w3_64"], d["w2_64"], top, wts, h_rel=2.0 ** -8)
+    R.check(yg[:-1], y, tol, "few")
+    R.check(y2, y, tol, "full", extra=2.0 ** -8)
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_few_given_routing(mx4):
+    """Given experts and weights: ids out of range add nothing (a token with none gets zeros),
+    repeats count twice, all tokens may share one expert; status bits are OR-ed in."""
+    T, h, f, E, k = shape = (40, 384, 256, 6, 3)
+    d = make(shape, seed=7, mx4=mx4)
+    g = torch.Generator().manual_seed(5)
+    top = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).cuda()
+    wts = torch.rand((T, k), generator=g).cuda()
+    for kind, bits in (("plain", 0), ("one expert", B.STATUS_DUPLICATE_EXPERT),
+                       ("absent", B.STATUS_EXPERT_OUT_OF_RANGE)):
+        t = top.clone()
+        if kind == "one expert":  # 3 x 40 entries at expert 4: every token three times
+            t[:] = 4
+        if kind == "absent":
+            t[3] = torch.tensor([-1, E, 2 ** 31 - 1])
+            t[5, 1] = -2 ** 31
+            t[T - 1, 0] = E + 5
+        bufs, yg = outputs(d)
+        bufs.status.fill_(B.STATUS_TIMEOUT)
+        bufs.top_experts.copy_(t)
+        bufs.weights.copy_(wts)
+        run(d, bufs, yg[:-1], logits=None)
+        torch.cuda.synchronize()
+        assert int(bufs.status.item()) == bits | B.STATUS_TIMEOUT, kind
+        assert torch.equal(bufs.top_experts.long(), t) and torch.equal(bufs.weights, wts)
+        y, tol = reference(d, t, wts)
+        R.check(yg[:-1], y, tol, kind)
+        if kind == "absent":
+            assert (yg[3] == 0).all()
+
+
+def test_few_every_entry_absent():
+    d = make((5, 256, 128, 4, 2))
+    bufs, yg = outputs(d)
+    bufs.top_experts.fill_(-1)
+    bufs.weights.fill_(1.0)
+    run(d, bufs, yg[:-1], logits=None)
+    torch.cuda.synchronize()
+    assert (yg[:-1] == 0).all() and (yg[-1] == 7.0).all()
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_few_nonfinite_rows_stay_in_their_rows(mx4):
+    """An inf or NaN in one token's x shows in that token's y and nowhere else; weights of
+    experts that nobody chose are not read into any result; tiny and huge x keep their size."""
+    T, h, f, E, k = shape = (11, 256, 256, 8, 2)
+    d = make(shape, seed=9, mx4=mx4)
+    top = torch.tensor([[(2 * t) % 6, (2 * t + 1) % 6] for t in range(T)]).cuda()
+    if mx4:
+        d["w1"].scales[6:] = 255
+        d["w2"].scales[6:] = 255
+    else:
+        d["w1"][6:] = float("nan")
+        d["w2"][6:] = float("inf")
+    d["x"][2, 17] = float("nan")
+    d["x"][5, 200] = float("inf")
+    d["x"][7] *= 2.0 ** -60
+    d["x"][8] *= 2.0 ** 40
+    d["x"][9] = 0
+    bufs, yg = outputs(d)
+    bufs.top_experts.copy_(top)
+    bufs.weights.fill_(0.5)
+    run(d, bufs, yg[:-1], logits=None)
+    torch.cuda.synchronize()
+    y, tol = reference(d, top, bufs.weights.double())
+    fine = [t for t in range(T) if t not in (2, 5)]
+    R.check(yg[fine], y[fine], tol[fine], "finite rows")
+    assert not torch.isfinite(yg[[2, 5]].float()).any()
+    assert (yg[9] == 0).all()
+
+
+def test_few_nonfinite_logits():
+    """NaN ranks last; the status says so; the routing stays in range (as dmoe_sparse_map)."""
+    T, h, f, E, k = shape = (6, 128, 128, 8, 3)
+    d = make(shape, seed=11)
+    d["logits"][1, 2] = float("nan")
+    d["logits"][2] = float("nan")
+    d["logits"][3, 5] = float("-inf")
+    bufs, yg = outputs(d)
+    run(d, bufs, yg[:-1])
+    full = B.Buffers(d["dims"])
+    B.dmoe_sparse_map(d["dims"], d["logits"], full.map, full.ws_map)
+    torch.cuda.synchronize()
+    assert int(bufs.status.item()) == B.STATUS_NONFINITE_LOGITS == int(full.map.status.item())
+    assert torch.equal(bufs.top_experts, full.map.top_experts)
+    ok = [0, 3, 4, 5]
+    assert torch.allclose(bufs.weights[ok], full.map.weights[ok], rtol=2e-6, atol=0)
+    assert torch.isnan(bufs.weights[1:3]).all() and torch.isnan(full.map.weights[1:3]).all()
+    assert torch.isfinite(yg[ok].float()).all()
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_few_two_streams_and_graph(mx4):
+    """Two calls in flight on two streams, each with its own buffers; then both captured in one
+    graph and replayed on new inputs: the eager results bit for bit."""
+    ds = [make((13, 512, 256, 32, 4), seed=s, mx4=mx4) for s in (1, 2)]
+    eager = []
+    for d in ds:
+        bufs, yg = outputs(d)
+        run(d, bufs, yg[:-1])
+        eager.append(yg)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    bufs_y = [outputs(d) for d in ds]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, s, (bufs, yg) in zip(ds, streams, bufs_y):
+            run(d, bufs, yg[:-1], stream=s)
+    torch.cuda.synchronize()
+    for e, (_, yg) in zip(eager, bufs_y):
+        assert same(e, yg)
+    # one workspace for both calls, one after the other in a captured graph
+    shared, _ = outputs(ds[0])
+    ys = [torch.empty_like(d["x"]) for d in ds]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for d, y in zip(ds, ys):
+            run(d, shared, y)
+    for r in range(3):
+        for d in ds:
+            d["x"].copy_(torch.roll(d["x"], 1, 0))
+            d["logits"].copy_(torch.roll(d["logits"], 1, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        for d, y in zip(ds, ys):
+            bufs, yg = outputs(d)
+            run(d, bufs, yg[:-1])
+            torch.cuda.synchronize()
+            assert same(yg[:-1], y), r
+
+
+@pytest.mark.parametrize("E,k", [(12, 3), (32, 32), (256, 8), (1024, 8)])
+def test_few_decode_loop_follows_its_router(E, k):
+    """A decode step as a model runs it: router, few-token layer, residual, several steps."""
+    T, h, f = 5, 256, 128
+    d = make((T, h, f, E, k), seed=E, wscale=0.02)
+    bufs = B.FewBuffers(d["dims"])
+    y = torch.empty_like(d["x"])
+    for step in range(4):
+        run(d, bufs, y)
+        top, wts = R.route(d["logits"], k)
+        ref, tol = reference(d, top, wts)
+        R.check(y, ref, tol, f"step {step}")
+        d["x"].copy_((d["x"].float() + y.float()).bfloat16())
+        d["logits"].copy_(torch.roll(d["logits"], 1, 1))
+    assert int(bufs.status.item()) == 0
