@@ -759,41 +759,17 @@ int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t *w = static_cast<uint8_t *>(ws);
   float *yscale = reinterpret_cast<float *>(w + l.yscale);
-  const long long max_blocks = pmax_of(dims) / DMOE_BLOCKING;
   if ((rc = launch_rc(launch_mx4_gather(dims->T, dims->hidden, dims->top_k, dims->num_experts, x,
                                         map->dest_row, map->tokens_per_expert, map->padded_bins,
                                         w + l.xq, w + l.xs, st, entry_offsets_of(dims, map)))))
     return rc;
-  Mx4GemmParams p;
-  p.E = dims->num_experts;
-  p.h = dims->hidden;
-  p.f = dims->ffn;
-  p.num_blocks = map->num_blocks;
-  p.block_expert = map->block_expert;
-  p.padded_bins = map->padded_bins;
-  p.bins = map->bins;
-  p.indices = map->indices;
-  p.weights = map->weights;
-  p.status = map->status;
-  p.a = w + l.xq;
-  p.as = w + l.xs;
-  p.w1 = static_cast<const uint8_t *>(w1->codes);
-  p.w1s = static_cast<const uint8_t *>(w1->scales);
-  p.w3 = static_cast<const uint8_t *>(w3->codes);
-  p.w3s = static_cast<const uint8_t *>(w3->scales);
-  p.out = w + l.hq;
-  p.outs = w + l.hs;
-  p.yscale = nullptr;
-  if ((rc = launch_rc(launch_mx4_glu(p, max_blocks, st)))) return rc;
-  p.a = w + l.hq;
-  p.as = w + l.hs;
-  p.w1 = static_cast<const uint8_t *>(w2->codes);
-  p.w1s = static_cast<const uint8_t *>(w2->scales);
-  p.w3 = p.w3s = nullptr;
-  p.out = w + l.ypad;
-  p.outs = nullptr;
-  p.yscale = yscale;
-  if ((rc = launch_rc(launch_mx4_down(p, max_blocks, st)))) return rc;
+  const GemmProblem g = problem_of(dims, map);
+  if ((rc = launch_rc(launch_mx4_glu(g, w + l.xq, w + l.xs, w1->codes, w1->scales, w3->codes,
+                                     w3->scales, w + l.hq, w + l.hs, st))))
+    return rc;
+  if ((rc = launch_rc(launch_mx4_down(g, w + l.hq, w + l.hs, w2->codes, w2->scales, w + l.ypad,
+                                      yscale, st))))
+    return rc;
   return dmoe_padded_scatter(dims, w + l.ypad, yscale, map, nullptr, y, stream);  // rows weighted
 }
 

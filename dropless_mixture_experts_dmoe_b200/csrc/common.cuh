@@ -414,4 +414,13 @@ __device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.0f + _
 // sigmoid(z) = 1 / (1 + e^-z), same intrinsics.
 __device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+// ---- host ------------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled of the driver in use (NULL if it has none), looked up once (gemm.cu).
+EncodeTiledFn get_encode_fn();
+
 }  // namespace dmoe

@@ -1087,12 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<MODE, EPI>::thre
 
 // ---- host side -------------------------------------------------------------------------------
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn get_encode_fn() {
+EncodeTiledFn get_encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -1165,12 +1160,13 @@ static int raster_units(int K) {
 static std::atomic<int> g_inject_stall{0};
 
 void set_inject_stall(int on) { g_inject_stall.store(on ? 1 : 0); }
+int take_inject_stall() { return g_inject_stall.exchange(0); }
 
 template <int MODE, int EPI>
 static cudaError_t launch_gemm(const GemmParams &p_in, long long max_tiles, cudaStream_t st) {
   using C = Cfg<MODE, EPI>;
   GemmParams p = p_in;
-  p.inject = g_inject_stall.exchange(0);
+  p.inject = take_inject_stall();
   p.wait_cycles = p.inject ? kInjectedWaitCycles : kWaitCycles;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;

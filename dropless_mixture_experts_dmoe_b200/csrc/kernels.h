@@ -185,24 +185,18 @@ cudaError_t launch_mx4_dequantize(long long rows, long long cols, const void *co
 cudaError_t launch_mx4_gather(int T, int h, int k, int E, const void *x, const int32_t *dest_row,
                               const int32_t *counts, const int32_t *padded_bins, void *codes,
                               void *scales, cudaStream_t st, const int32_t *offsets);
-struct Mx4GemmParams {
-  int E, h, f;
-  const int32_t *num_blocks, *block_expert, *padded_bins, *bins, *indices;
-  const float *weights;
-  const uint8_t *a, *as;    // left operand [P_max, K] in the format
-  const uint8_t *w1, *w1s;  // W1 (GLU) or W2 (DOWN)
-  const uint8_t *w3, *w3s;  // W3 (GLU)
-  uint8_t *out;             // GLU: H elements [P_max, f / 2]; DOWN: Y_pad [P_max, h] fp16
-  uint8_t *outs;            // GLU: scales of H
-  float *yscale;            // DOWN: scales of Y_pad's rows
-  int32_t *status;
-};
-cudaError_t launch_mx4_glu(const Mx4GemmParams &p, long long max_blocks, cudaStream_t st);
-cudaError_t launch_mx4_down(const Mx4GemmParams &p, long long max_blocks, cudaStream_t st);
+// GLU: X_pad in the format -> H [P_max, f] in the format (converted from fp32).  DOWN: H in the
+// format -> Y_pad in block floating point, rows weighted (as launch_down_gemm).
+cudaError_t launch_mx4_glu(const GemmProblem &g, const void *xq, const void *xs, const void *w1,
+                           const void *s1, const void *w3, const void *s3, void *hq, void *hs,
+                           cudaStream_t st);
+cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs, const void *w2,
+                            const void *s2, void *y_pad, float *y_scale, cudaStream_t st);
 
 int device_sm_count();
 
 // Test-only: make the next grouped-GEMM launch stall on purpose (see dmoe_debug_inject_stall).
 void set_inject_stall(int on);
+int take_inject_stall();  // what is set, cleared
 
 }  // namespace dmoe
