@@ -230,9 +230,20 @@ void saved_layout(const dmoe_dims *d, size_t off[3], size_t *total) {
   *total = align_up(off[2] + P * d->ffn * 2);
 }
 
-// Few-token workspace: H [T*k, f] fp32.
-inline size_t few_bytes(const dmoe_dims *d) {
-  return align_up((size_t)d->T * d->top_k * d->ffn * sizeof(float));
+// Few-token workspace: H [T*k, f] upper bf16 (or fp16) | its lower bf16 (or the fp16 blocks'
+// scales [T*k, f/32] fp32) | x [T, h] in fp16 | its scales [T, h/32] fp32
+struct FewLayout {
+  size_t h, lo, x16, xs, total;
+};
+FewLayout few_layout(const dmoe_dims *d) {
+  const size_t n = (size_t)d->T * d->top_k * d->ffn, x = (size_t)d->T * d->hidden;
+  FewLayout l;
+  l.h = 0;
+  l.lo = align_up(l.h + n * 2);
+  l.x16 = align_up(l.lo + n * 2);
+  l.xs = align_up(l.x16 + x * 2);
+  l.total = align_up(l.xs + x / 32 * sizeof(float));
+  return l;
 }
 
 inline int check_few_dims(const dmoe_dims *d) {
@@ -257,13 +268,15 @@ int forward_few(const dmoe_dims *dims, const void *x, const void *logits, FewWei
                 FewWeights w3, FewWeights w2, int32_t *top, float *weights, void *y,
                 int32_t *status, void *ws, size_t ws_bytes, void *stream) {
   if (!x || !top || !weights || !y || !status || !ws) return DMOE_ERR_NULL;
-  if (ws_bytes < few_bytes(dims)) return DMOE_ERR_WORKSPACE;
+  const FewLayout l = few_layout(dims);
+  if (ws_bytes < l.total) return DMOE_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(logits) || !aligned16(top) || !aligned16(weights) ||
       !aligned16(y) || !aligned16(ws))
     return DMOE_ERR_ALIGN;
   int rc = check_device();
   if (rc) return rc;
-  FewParams p;
+  uint8_t *b = static_cast<uint8_t *>(ws);
+  FewParams p = {};
   p.T = dims->T;
   p.k = dims->top_k;
   p.E = dims->num_experts;
@@ -275,8 +288,16 @@ int forward_few(const dmoe_dims *dims, const void *x, const void *logits, FewWei
   p.w2 = w2;
   p.top = top;
   p.weights = weights;
-  p.hbuf = static_cast<float *>(ws);
+  p.given = logits == nullptr;
   p.y = static_cast<__nv_bfloat16 *>(y);
+  p.hout = reinterpret_cast<uint16_t *>(b + l.h);
+  if (w1.scales) {
+    p.hscale = reinterpret_cast<float *>(b + l.lo);
+    p.x16 = reinterpret_cast<uint16_t *>(b + l.x16);
+    p.x16scale = reinterpret_cast<float *>(b + l.xs);
+  } else {
+    p.hlo = reinterpret_cast<uint16_t *>(b + l.lo);
+  }
   return launch_rc(launch_few(p, static_cast<const uint16_t *>(logits),
                               (dims->flags & DMOE_ROUTE_RENORMALIZE) != 0, top, weights, status,
                               static_cast<cudaStream_t>(stream)));
@@ -336,7 +357,7 @@ size_t dmoe_workspace_bytes(const dmoe_dims *dims, int kind) {
     case DMOE_WS_BACKWARD:
       return bwd_layout(dims).total;
     case DMOE_WS_FEW:
-      return check_few_dims(dims) == DMOE_OK ? few_bytes(dims) : 0;
+      return check_few_dims(dims) == DMOE_OK ? few_layout(dims).total : 0;
     case DMOE_WS_MX4_FORWARD:
       return mx4_layout(dims).total;
     default:

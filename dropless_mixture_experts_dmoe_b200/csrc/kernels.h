@@ -166,12 +166,20 @@ struct FewWeights {
 };
 struct FewParams {
   int T, k, E, h, f;
+  bool given;     // the experts are the caller's: they may repeat within a token
   const void *x;  // [T, h] bf16
   FewWeights w1, w3, w2;
   const int32_t *top;    // [T, k]
   const float *weights;  // [T, k]
-  float *hbuf;           // [T*k, f]
   __nv_bfloat16 *y;      // [T, h]
+  // workspace: H [T*k, f] as bf16 + bf16, or (4-bit weights) as fp16 with a scale per 32 columns,
+  // and x [T, h] in that form
+  uint16_t *hout, *hlo, *x16;
+  float *hscale, *x16scale;
+  // set by launch_few for each product: its token operand, and CTAs per row tile
+  const uint16_t *xin, *xlo;
+  const float *xscale;
+  int groups;
 };
 // logits given: top and weights are written first; else they are inputs.
 cudaError_t launch_few(const FewParams &p, const uint16_t *logits, bool renorm, int32_t *top,
