@@ -231,7 +231,7 @@ void saved_layout(const dmoe_dims *d, size_t off[3], size_t *total) {
 }
 
 // Few-token workspace: H [T*k, f] upper bf16 (or fp16) | its lower bf16 (or the fp16 blocks'
-// scales [T*k, f/32] fp32) | x [T, h] in fp16 | its scales [T, h/32] fp32
+// scales [T*k, f/32] fp32) | x [T, h] in fp16 | its scales [T] fp32
 struct FewLayout {
   size_t h, lo, x16, xs, total;
 };
@@ -242,7 +242,7 @@ FewLayout few_layout(const dmoe_dims *d) {
   l.lo = align_up(l.h + n * 2);
   l.x16 = align_up(l.lo + n * 2);
   l.xs = align_up(l.x16 + x * 2);
-  l.total = align_up(l.xs + x / 32 * sizeof(float));
+  l.total = align_up(l.xs + (size_t)d->T * sizeof(float));
   return l;
 }
 

@@ -16,10 +16,12 @@
 // tile into the next, across experts.  tcgen05 would need 128-row tiles and a full shared-memory
 // operand for 1 to 8 columns, and the 4-bit weights converted into it.
 //   bf16 weights: x as bf16; H as the sum of two bf16 (16 bits), multiplied in turn.
-//   4-bit weights: e2m1 -> fp16 is exact, so x and H go in fp16 under a power-of-two scale per
-//     row and 32 columns (11 bits at the block's largest, exact for x down to 2^-29 of it);
-//     the 32 products of a block are summed first, then scaled by the block's two scales.
+//   4-bit weights: e2m1 -> fp16 is exact, so x and H go in fp16 under a power-of-two scale, x per
+//     row (exact down to 2^-29 of the row's largest), H per 32 columns (11 bits); the 32
+//     products of a weight block are summed first, then scaled by the block's scale.
 // The few partial sums over S and over the experts of a token are added in a fixed order.
+#include <stdlib.h>
+
 #include <atomic>
 
 #include "common.cuh"
@@ -106,41 +108,52 @@ __device__ __forceinline__ void check_token(const int32_t *__restrict__ top, int
   if (flags && lane == 0) set_status(status, flags);
 }
 
-// One CTA per token: warp 0 routes (or checks) it, the others convert its row of x to fp16 when
-// the weights have four bits.
+// One CTA per token: warp 0 routes (or checks) it; when the weights have four bits the other
+// warps convert its row of x to fp16 under one power-of-two scale.
 __global__ void __launch_bounds__(32 * kRouteWarps)
     k_few_route(const uint16_t *__restrict__ logits, int E, int k, int renorm, int h,
                 int32_t *__restrict__ top, float *__restrict__ weights, int32_t *status,
                 const uint4 *__restrict__ x, uint4 *__restrict__ x16, float *__restrict__ xs) {
+  __shared__ uint32_t s_max;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t t = blockIdx.x;
+  const int vpr = h >> 3;
+  if (x16) {
+    if (threadIdx.x == 0) s_max = 0u;
+    __syncthreads();
+    if (warp > 0) {
+      uint32_t m = 0u;
+      for (int v = threadIdx.x - 32; v < vpr; v += 32 * (kRouteWarps - 1)) {
+        const uint4 q = __ldg(x + t * vpr + v);
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = max(m, max(finite_abs(w[i] << 16), finite_abs(w[i] & 0xFFFF0000u)));
+      }
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (lane == 0) atomicMax(&s_max, m);
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
     if (logits)
       route_token(logits + t * E, E, k, renorm != 0, top + t * k, weights + t * k, status, lane);
     else
       check_token(top + t * k, E, k, status, lane);
   } else if (x16) {
-    const int vpr = h >> 3;  // h is a multiple of 128: whole lane groups of four per block
+    const int es = f16_block_exp(s_max);
+    const float f = pow2(es);
+    if (threadIdx.x == 32) xs[t] = pow2(-es);
     for (int v = threadIdx.x - 32; v < vpr; v += 32 * (kRouteWarps - 1)) {
       const uint4 q = __ldg(x + t * vpr + v);
       const uint32_t *w = reinterpret_cast<const uint32_t *>(&q);
-      uint32_t m = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m = max(m, max(finite_abs(w[i] << 16), finite_abs(w[i] & 0xFFFF0000u)));
-      const unsigned grp = 0xFu << (lane & 28);  // the block's four lanes
-      m = max(m, __shfl_xor_sync(grp, m, 1));
-      m = max(m, __shfl_xor_sync(grp, m, 2));
-      const int es = f16_block_exp(m);
-      const float f = pow2(es);
       uint4 o;
       uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ow[i] = pack_f16x2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
       x16[t * vpr + v] = o;
-      if ((lane & 3) == 0) xs[t * (h >> 5) + (v >> 2)] = pow2(-es);
     }
   }
 }
@@ -186,40 +199,55 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Shape of a variant: MX4 weights in four bits; NT tiles of 8 tokens; R x S warps; P stages;
-// DOWN the second product.  BR: copies of the token rows (two: H's upper and lower bf16).
-template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int P_>
+// Shape of a variant: MX4 weights in four bits; DOWN the second product; NT tiles of 8 tokens;
+// R x S warps of KU columns; P stages.  BR: copies of the token rows (two: H's upper and lower
+// bf16).  SB: the token operand has a scale per 32 columns (H in fp16).
+template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int KU_, int P_>
 struct FewCfg {
-  static constexpr bool MX4 = MX4_, DOWN = DOWN_;
-  static constexpr int NT = NT_, R = R_, S = S_, P = P_;
+  static constexpr bool MX4 = MX4_, DOWN = DOWN_, SB = MX4 && DOWN;
+  static constexpr int NT = NT_, R = R_, S = S_, KU = KU_, P = P_;
   static constexpr int warps = R * S, threads = 32 * warps;
   static constexpr int min_ctas = threads == 256 ? 2 : 1;
-  static constexpr int KU = MX4 ? 128 : 64;  // columns per warp and stage
-  static constexpr int CH = S * KU;          // columns per stage
+  static constexpr int CH = S * KU;  // columns per stage
   static constexpr int BR = (DOWN && !MX4) ? 2 : 1;
-  static constexpr int w_warp = MX4 ? 1024 : 2048;  // weight bytes per warp and stage
-  static constexpr int sc_warp = MX4 ? 256 : 0;     // weight scales: 16 bytes per row
+  static constexpr int wbits = MX4 ? 4 : 16;
+  static constexpr int w_warp = 16 * KU * wbits / 8;       // weight bytes per warp and stage
+  static constexpr int sc_warp = MX4 ? KU / 128 * 256 : 0;  // scales: 16 bytes per row and 128 K
   // token rows: a stride that is 16 (ldmatrix) or 64 (16-byte loads of 4 lanes a row) bytes off
   // a multiple of 128 keeps the reads free of bank conflicts
   static constexpr int x_row = CH * 2 + (MX4 ? 64 : 16);
   static constexpr int x_bytes = BR * 8 * NT * x_row;
-  static constexpr int sb_bytes = MX4 ? (CH / 32) * 8 * NT * 4 : 0;  // token scales [block][token]
+  static constexpr int sb_bytes = SB ? (CH / 32) * 8 * NT * 4 : 0;  // token scales [block][token]
   static constexpr int o_sc = warps * w_warp, o_x = o_sc + warps * sc_warp, o_sb = o_x + x_bytes;
   static constexpr int stage = o_sb + sb_bytes;
-  // partial sums of every warp; with two slices of K the first slice's warps add theirs to the
-  // second's in place
-  static constexpr int red_s = S == 2 ? 1 : S;
-  static constexpr int red = R * red_s * NT * 512;
-  static constexpr int rows = 16 * R;           // weight rows per tile
+  static constexpr int rows = 16 * R;                  // weight rows per tile
   static constexpr int outs = DOWN ? rows : rows / 2;  // output columns per tile
-  static_assert(stage % 128 == 0 && o_x % 16 == 0 && x_row % 16 == 0, "alignment");
+  // partial sums: of the slices of K past the first, and for GLU MX4 a tile's H in fp32
+  static constexpr int red = (S - 1) * R * NT * 512;
+  static constexpr int hrow = outs + 4;
+  static constexpr int hbuf = (MX4 && !DOWN) ? 8 * NT * hrow * 4 : 0;
+  // y sums: rows of `outs` plus 8 floats (four tokens x eight rows meet no bank twice)
+  static constexpr int yrow = outs + 8;
+  static constexpr int o_red = P * stage, o_hbuf = o_red + red, o_lists = o_hbuf + hbuf;
+  static_assert(stage % 16 == 0 && o_x % 16 == 0 && x_row % 16 == 0, "alignment");
+  static_assert(!MX4 || DOWN || outs % 32 == 0, "whole blocks of H");
 };
 
-// Bytes of the expert lists: counts / starts [E + 1] int, active experts and entries (uint16).
+// Bytes of the expert lists: entries [n] (j | token << 16), starts [E + 1], experts in use
+// (uint16).
 __host__ __device__ inline size_t few_list_bytes(int E, int n) {
-  const size_t a = (size_t)(E + 1) * 4 + (size_t)(E < n ? E : n) * 2 + (size_t)n * 2 + 8;
+  const size_t a = (size_t)n * 4 + (size_t)(E + 1) * 4 + (size_t)(E < n ? E : n) * 2;
   return (a + 15) / 16 * 16;
 }
+
+struct FewLists {
+  uint32_t *ent;
+  int *start;
+  uint16_t *act;
+  __device__ __forceinline__ FewLists(uint8_t *base, int E, int n)
+      : ent(reinterpret_cast<uint32_t *>(base)), start(reinterpret_cast<int *>(ent + n)),
+        act(reinterpret_cast<uint16_t *>(start + E + 1)) {}
+};
 
 // Expert of entry j, or -1 for one that is not listed: an id outside [0, E), or an expert that an
 // earlier slot of the token names too (its weights are added up, see few_weight).  Read through
@@ -242,13 +270,13 @@ __device__ __forceinline__ float few_weight(const FewParams &p, int j, int e) {
   return w;
 }
 
-// The experts in use, in increasing order, and their entries.  start[e] .. start[e + 1] are e's entries in ent; returns the number of
-// experts in use.  An entry's place in its expert's list decides only which column of the
-// product it is, so the order the atomics give does not show in any result.
+// The experts in use, in increasing order, and their entries: start[e] .. start[e + 1] in ent.
+// Returns the number of experts in use.  An entry's place in its expert's list decides only
+// which column of the product it is, so the order the atomics give does not show in any result.
 template <int THREADS>
-__device__ __forceinline__ int few_lists(const FewParams &p, int *start, uint16_t *act,
-                                         uint16_t *ent, int *s_act) {
+__device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, int *s_act) {
   const int n = p.T * p.k, lane = threadIdx.x & 31;
+  int *start = l.start;
   for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = 0;
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
@@ -268,7 +296,7 @@ __device__ __forceinline__ int few_lists(const FewParams &p, int *start, uint16_
         const int u = __shfl_up_sync(0xFFFFFFFFu, v, off);
         if (lane >= off) v += u;
       }
-      if (c > 0) act[na + __popc(on & ((1u << lane) - 1u))] = (uint16_t)e;
+      if (c > 0) l.act[na + __popc(on & ((1u << lane) - 1u))] = (uint16_t)e;
       if (e < p.E) start[e] = carry + v;
       na += __popc(on);
       carry += __shfl_sync(0xFFFFFFFFu, v, 31);
@@ -281,7 +309,7 @@ __device__ __forceinline__ int few_lists(const FewParams &p, int *start, uint16_
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
     const int e = few_entry(p, j);
-    if (e >= 0) ent[atomicSub(&start[e], 1) - 1] = (uint16_t)j;
+    if (e >= 0) l.ent[atomicSub(&start[e], 1) - 1] = (uint32_t)j | ((uint32_t)(j / p.k) << 16);
   }
   __syncthreads();  // start[e] is now the first entry of e
   return *s_act;
@@ -296,22 +324,29 @@ struct FewPos {
 template <class C>
 struct FewKernel {
   const FewParams &p;
-  const int *start;
-  const uint16_t *act, *ent;
+  const FewLists &l;
   uint32_t ring;
   int warp, lane, r, s;
   int K, chunks, tiles;
   int item_end, item_step;  // GLU: items are (expert, tile) pairs; DOWN: experts of one tile
   int fixed_tile;
+  // this lane's rows of the tile being loaded (rows 0..7 in a, 8..15 in b), at its slice of K
+  const uint8_t *wa, *wb, *ws;
+
+  __device__ __forceinline__ FewKernel(const FewParams &p_, const FewLists &l_, uint32_t ring_)
+      : p(p_), l(l_), ring(ring_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
+        r(warp / C::S), s(warp % C::S), K(C::DOWN ? p_.f : p_.h), chunks((K + C::CH - 1) / C::CH),
+        tiles(C::DOWN ? p_.h / C::rows : p_.f / (C::rows / 2)), item_end(0), item_step(1),
+        fixed_tile(0), wa(nullptr), wb(nullptr), ws(nullptr) {}
 
   __device__ __forceinline__ void open(FewPos &q) const {
     q.on = q.item < item_end;
     if (!q.on) return;
     const int a = C::DOWN ? q.item : q.item / tiles;
     q.tile = C::DOWN ? fixed_tile : q.item - a * tiles;
-    q.e = act[a];
-    q.n0 = start[q.e];
-    q.cnt = start[q.e + 1] - q.n0;
+    q.e = l.act[a];
+    q.n0 = l.start[q.e];
+    q.cnt = l.start[q.e + 1] - q.n0;
     q.chunk = 0;
   }
   __device__ __forceinline__ void next(FewPos &q) const {
@@ -326,40 +361,65 @@ struct FewKernel {
     open(q);
   }
 
-  // This warp's 16 weight rows of the stage.
-  __device__ __forceinline__ void load_w(const FewPos &q, int st) const {
-    const int k0 = q.chunk * C::CH + s * C::KU;
-    if (k0 >= K) return;
-    const uint32_t dst = ring + st * C::stage + warp * C::w_warp;
-    const FewWeights &wa = C::DOWN ? p.w2 : p.w1;
-    const FewWeights &wb = C::DOWN ? p.w2 : p.w3;
-    const long long row0 = C::DOWN ? (long long)q.e * p.h + q.tile * C::rows + r * 16
-                                   : (long long)q.e * p.f + q.tile * (C::rows / 2) + r * 8;
-    const long long rb0 = C::DOWN ? row0 + 8 : row0;  // rows 8..15
-    if constexpr (C::MX4) {
-      const int rr = lane >> 2, seg = lane & 3;
-      const size_t col = (size_t)(k0 >> 1) + seg * 16;
-      const uint32_t d = dst + rr * 64 + ((seg ^ ((rr >> 1) & 3)) << 4);
-      cp16(d, static_cast<const uint8_t *>(wa.data) + (size_t)(row0 + rr) * (K >> 1) + col);
-      cp16(d + 512, static_cast<const uint8_t *>(wb.data) + (size_t)(rb0 + rr) * (K >> 1) + col);
-      if (lane < 16) {  // the 16-byte piece with the row's word in it (past L1, as the elements)
-        const FewWeights &w = lane < 8 ? wa : wb;
-        const long long row = (lane < 8 ? row0 : rb0) + (lane & 7);
-        cp16(ring + st * C::stage + C::o_sc + warp * C::sc_warp + lane * 16,
-             static_cast<const uint8_t *>(w.scales) +
-                 (mx4_scale_word(row, k0 >> 7, K >> 7) & ~(size_t)15));
-      }
+  // Row 0 (a) and row 8 (b) of this warp's 16 in the tile.
+  __device__ __forceinline__ void rows_of(const FewPos &q, long long &a, long long &b) const {
+    if (C::DOWN) {
+      a = (long long)q.e * p.h + q.tile * C::rows + r * 16;
+      b = a + 8;
     } else {
-      const int rr = lane >> 3, seg = lane & 7;
+      a = b = (long long)q.e * p.f + q.tile * (C::rows / 2) + r * 8;
+    }
+  }
+
+  // This warp's 16 weight rows of the stage.
+  __device__ __forceinline__ void load_w(const FewPos &q, int st) {
+    constexpr int seg_lanes = C::MX4 ? C::KU / 32 : 8;  // lanes (16 bytes each) per row
+    constexpr int row_step = 32 / seg_lanes;
+    const int rr = lane / seg_lanes, seg = lane % seg_lanes;
+    const size_t pitch = (size_t)K * C::wbits / 8;
+    if (q.chunk == 0) {
+      const FewWeights &fa = C::DOWN ? p.w2 : p.w1;
+      const FewWeights &fb = C::DOWN ? p.w2 : p.w3;
+      long long a, b;
+      rows_of(q, a, b);
+      const size_t col = (size_t)s * C::KU * C::wbits / 8 + seg * 16;
+      wa = static_cast<const uint8_t *>(fa.data) + (size_t)(a + rr) * pitch + col;
+      wb = static_cast<const uint8_t *>(fb.data) + (size_t)(b + rr) * pitch + col;
+      if (C::MX4 && lane < 16)  // the 16-byte piece with the row's word in it (past L1)
+        ws = static_cast<const uint8_t *>(lane < 8 ? fa.scales : fb.scales) +
+             (mx4_scale_word((lane < 8 ? a : b) + (lane & 7), s * (C::KU / 128), K >> 7) &
+              ~(size_t)15);
+    }
+    const int left = K - q.chunk * C::CH - s * C::KU;  // a multiple of 64 (4 bits: of 128)
+    if (left > 0) {
+      const uint32_t dst = ring + st * C::stage + warp * C::w_warp;
+      if (seg * (C::MX4 ? 32 : 8) < left) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + rr;
-        const FewWeights &w = i < 2 ? wa : wb;
-        const long long g = (i < 2 ? row0 : rb0) + (row & 7);
-        cp16(dst + row * 128 + ((seg ^ (row & 7)) << 4),
-             static_cast<const uint16_t *>(w.data) + (size_t)g * K + k0 + seg * 8);
+        for (int i = 0; i < 8; i += row_step) {
+          const int row = i + rr;
+          const uint32_t d = dst + row * (seg_lanes * 16) + (swz(row, seg) << 4);
+          cp16(d, wa + i * pitch);
+          cp16(d + 8 * seg_lanes * 16, wb + i * pitch);
+        }
+      }
+      if (C::MX4 && lane < 16) {
+        const uint32_t d = ring + st * C::stage + C::o_sc + warp * C::sc_warp + lane * 16;
+#pragma unroll
+        for (int j = 0; j < C::KU / 128; ++j)
+          if (j * 128 < left) cp16(d + 256 * j, ws + kMx4TileBytes * j);
       }
     }
+    wa += C::CH * C::wbits / 8;
+    wb += C::CH * C::wbits / 8;
+    ws += (C::CH / 128) * kMx4TileBytes;
+  }
+
+  // Place of 16-byte piece `seg` of a weight row in its row of the stage.  bf16: ldmatrix reads
+  // one piece of eight rows.  4 bits: eight rows' four words of a piece (32 lanes) are read; rows
+  // of 64 bytes share their banks with every second row, rows of 128 bytes with every row.
+  __device__ __forceinline__ static int swz(int row, int seg) {
+    if (!C::MX4) return seg ^ (row & 7);
+    return C::KU == 128 ? seg ^ ((row >> 1) & 3) : seg ^ (row & 7);
   }
 
   // The token rows of the stage (columns past K are not loaded and not used).
@@ -371,21 +431,17 @@ struct FewKernel {
     for (int i = threadIdx.x; i < nr * segs; i += C::threads) {
       const int n = i / segs, seg = i % segs;
       if (c0 + seg * 8 >= K) continue;
-      const int j = ent[q.n0 + n];
-      const size_t row = C::DOWN ? (size_t)j : (size_t)(j / p.k);
-#pragma unroll
-      for (int b = 0; b < C::BR; ++b) {
-        const uint16_t *src = b ? p.xlo : p.xin;
-        cp16(dst + (b * 8 * C::NT + n) * C::x_row + seg * 16, src + row * K + c0 + seg * 8);
-      }
+      const uint32_t v = l.ent[q.n0 + n];
+      const size_t at = (size_t)(C::DOWN ? v & 0xFFFFu : v >> 16) * K + c0 + seg * 8;
+      cp16(dst + n * C::x_row + seg * 16, p.xin + at);
+      if (C::BR == 2) cp16(dst + (8 * C::NT + n) * C::x_row + seg * 16, p.xlo + at);
     }
-    if constexpr (C::MX4) {
+    if constexpr (C::SB) {
       constexpr int nb = C::CH / 32;
       for (int i = threadIdx.x; i < nr * nb; i += C::threads) {
         const int n = i / nb, b = i % nb;
         if (c0 + b * 32 >= K) continue;
-        const int j = ent[q.n0 + n];
-        const size_t row = C::DOWN ? (size_t)j : (size_t)(j / p.k);
+        const size_t row = l.ent[q.n0 + n] & 0xFFFFu;
         cp4(ring + st * C::stage + C::o_sb + (b * 8 * C::NT + n) * 4,
             p.xscale + row * (K >> 5) + (c0 >> 5) + b);
       }
@@ -393,7 +449,8 @@ struct FewKernel {
   }
 
   __device__ __forceinline__ void multiply(const FewPos &q, int st, float (&acc)[C::NT][4]) const {
-    if (q.chunk * C::CH + s * C::KU >= K) return;
+    const int left = K - q.chunk * C::CH - s * C::KU;
+    if (left <= 0) return;
     const uint32_t base = ring + st * C::stage;
     const uint32_t w = base + warp * C::w_warp;
     const int ntl = (min(q.cnt, 8 * C::NT) + 7) >> 3;
@@ -402,37 +459,49 @@ struct FewKernel {
       // rows 0..7 and 8..15 of a tile start at multiples of 8: one 32-row group each
       const int ra = q.tile * C::outs + r * (C::DOWN ? 16 : 8);
       const uint32_t sw = base + C::o_sc + warp * C::sc_warp + g * 16 + ((ra >> 5) & 3) * 4;
-      const uint32_t sca = lds32(sw), scb = lds32(sw + 128);
       const uint32_t xb = base + C::o_x + g * C::x_row + (s * C::KU + 8 * t) * 2;
       const uint32_t sb = base + C::o_sb + (s * (C::KU / 32) * 8 * C::NT + 2 * t) * 4;
+      constexpr int wrow = C::KU / 2;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint32_t wa = w + g * 64 + ((b ^ ((g >> 1) & 3)) << 4) + 4 * t;
-        uint32_t lo[4], hi[4];
-        mx4_unpack8(lds32(wa), lo);
-        mx4_unpack8(lds32(wa + 512), hi);
-        const float fa = mx4_scale_value((sca >> (8 * b)) & 0xFFu);
-        const float fb = mx4_scale_value((scb >> (8 * b)) & 0xFFu);
+      for (int j = 0; j < C::KU / 128; ++j) {
+        if (j * 128 >= left) break;
+        const uint32_t sca = lds32(sw + 256 * j), scb = lds32(sw + 256 * j + 128);
 #pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt) {
-          if (nt >= ntl) break;
-          uint32_t x0, x1, x2, x3;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                       : "r"(xb + nt * 8 * C::x_row + b * 64)
-                       : "memory");
-          float s0, s1;
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                       : "=f"(s0), "=f"(s1)
-                       : "r"(sb + (b * 8 * C::NT + nt * 8) * 4)
-                       : "memory");
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_f16(c, lo[0], hi[0], lo[1], hi[1], x0, x1);
-          mma_f16(c, lo[2], hi[2], lo[3], hi[3], x2, x3);
-          acc[nt][0] = fmaf(c[0] * s0, fa, acc[nt][0]);
-          acc[nt][1] = fmaf(c[1] * s1, fa, acc[nt][1]);
-          acc[nt][2] = fmaf(c[2] * s0, fb, acc[nt][2]);
-          acc[nt][3] = fmaf(c[3] * s1, fb, acc[nt][3]);
+        for (int b4 = 0; b4 < 4; ++b4) {
+          const int b = 4 * j + b4;
+          const uint32_t wl = w + g * wrow + (swz(g, b) << 4) + 4 * t;
+          uint32_t lo[4], hi[4];
+          mx4_unpack8(lds32(wl), lo);
+          mx4_unpack8(lds32(wl + 8 * wrow), hi);
+          const float fa = mx4_scale_value((sca >> (8 * b4)) & 0xFFu);
+          const float fb = mx4_scale_value((scb >> (8 * b4)) & 0xFFu);
+#pragma unroll
+          for (int nt = 0; nt < C::NT; ++nt) {
+            if (nt >= ntl) break;
+            uint32_t x0, x1, x2, x3;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                         : "r"(xb + nt * 8 * C::x_row + b * 64)
+                         : "memory");
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(c, lo[0], hi[0], lo[1], hi[1], x0, x1);
+            mma_f16(c, lo[2], hi[2], lo[3], hi[3], x2, x3);
+            if constexpr (C::SB) {
+              float s0, s1;
+              asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                           : "=f"(s0), "=f"(s1)
+                           : "r"(sb + (b * 8 * C::NT + nt * 8) * 4)
+                           : "memory");
+              c[0] *= s0;
+              c[1] *= s1;
+              c[2] *= s0;
+              c[3] *= s1;
+            }
+            acc[nt][0] = fmaf(c[0], fa, acc[nt][0]);
+            acc[nt][1] = fmaf(c[1], fa, acc[nt][1]);
+            acc[nt][2] = fmaf(c[2], fb, acc[nt][2]);
+            acc[nt][3] = fmaf(c[3], fb, acc[nt][3]);
+          }
         }
       }
     } else {
@@ -441,8 +510,8 @@ struct FewKernel {
 #pragma unroll
       for (int kk = 0; kk < 4; kk += 2) {
         uint32_t a0[4], a1[4];
-        ldsm4(a0, w + ar * 128 + (((2 * kk + (lane >> 4)) ^ (ar & 7)) << 4));
-        ldsm4(a1, w + ar * 128 + (((2 * kk + 2 + (lane >> 4)) ^ (ar & 7)) << 4));
+        ldsm4(a0, w + ar * 128 + (swz(ar, 2 * kk + (lane >> 4)) << 4));
+        ldsm4(a1, w + ar * 128 + (swz(ar, 2 * kk + 2 + (lane >> 4)) << 4));
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
           if (nt >= ntl) break;
@@ -459,35 +528,24 @@ struct FewKernel {
   }
 };
 
-// Element (row i of the tile, token n) of warp (r, s)'s sums in red: the accumulator of lane
-// 4 (i % 8) + n / 2, word 2 (i / 8) + n % 2.
-template <class C>
-__device__ __forceinline__ float red_sum(const float *red, int i16, int r, int n) {
-  const float *v = red + (((size_t)r * C::red_s) * C::NT + (n >> 3)) * 128 +
-                   (4 * (i16 & 7) + ((n & 7) >> 1)) * 4 + 2 * (i16 >> 3) + (n & 1);
-  float a = v[0];
-#pragma unroll
-  for (int q = 1; q < C::red_s; ++q) a += v[(size_t)q * C::NT * 128];
-  return a;
-}
-
-// The stream of stages that both products share.  PRE: issued before the wait for the earlier
-// kernels are the weight rows only.  done(pos): called by all threads when the sums of a
-// tile and entry group are in red.
-template <class C, class Done>
-__device__ __forceinline__ void few_stream(const FewKernel<C> &k, int item0, float *red,
-                                           bool pre, Done done) {
+// The stream of stages that both products share.  pre: before the wait for the earlier kernels
+// only weights are loaded.  done(pos, nt, sums): called by the first slice's warps with the
+// sums of token tile nt over all of K: words 2 i + c are row lane / 4 + 8 i of the warp's 16 and
+// token 8 nt + 2 (lane % 4) + c; end(pos): by all threads after them.
+template <class C, class Done, class End>
+__device__ __forceinline__ void few_stream(FewKernel<C> &k, int item0, float *red, bool pre,
+                                           Done done, End end) {
   FewPos pq;  // what is loaded next
   pq.item = item0;
   k.open(pq);
   FewPos cq = pq;
   if (pre) {  // weights of the first stages now, their token rows once the earlier kernel is done
-    FewPos w = pq;
+    FewPos xq = pq;
 #pragma unroll
     for (int i = 0; i < C::P - 1; ++i) {
-      if (w.on) {
-        k.load_w(w, i);
-        k.next(w);
+      if (pq.on) {
+        k.load_w(pq, i);
+        k.next(pq);
       }
       cp_commit();
     }
@@ -495,9 +553,9 @@ __device__ __forceinline__ void few_stream(const FewKernel<C> &k, int item0, flo
     pdl_trigger();
 #pragma unroll
     for (int i = 0; i < C::P - 1; ++i) {
-      if (pq.on) {
-        k.load_x(pq, i);
-        k.next(pq);
+      if (xq.on) {
+        k.load_x(xq, i);
+        k.next(xq);
       }
       cp_commit();
     }
@@ -532,34 +590,40 @@ __device__ __forceinline__ void few_stream(const FewKernel<C> &k, int item0, flo
     if (++st == C::P) st = 0;
     if (cq.chunk == k.chunks - 1) {
       const int ntl = (min(cq.cnt, 8 * C::NT) + 7) >> 3;
-      float4 *mine = reinterpret_cast<float4 *>(red) + k.lane +
-                     (size_t)(C::red_s == 1 ? k.r : k.warp) * C::NT * 32;
-      auto put = [&](bool add) {
+      // slices past the first hand over their sums (red is next written after the stage
+      // barrier of a later iteration)
+      float4 *part = reinterpret_cast<float4 *>(red) + k.r * C::NT * 32 + k.lane;
+      if (C::S > 1) {
+        if (k.s > 0) {
+#pragma unroll
+          for (int nt = 0; nt < C::NT; ++nt)
+            if (nt < ntl)
+              part[((k.s - 1) * C::R * C::NT + nt) * 32] =
+                  make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+        }
+        __syncthreads();
+      }
+      if (k.s == 0) {
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
           if (nt < ntl) {
-            float4 v = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-            if (add) {
-              const float4 o = mine[nt * 32];
-              v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+#pragma unroll
+            for (int q = 0; q < C::S - 1; ++q) {
+              const float4 v = part[(q * C::R * C::NT + nt) * 32];
+              acc[nt][0] += v.x;
+              acc[nt][1] += v.y;
+              acc[nt][2] += v.z;
+              acc[nt][3] += v.w;
             }
-            mine[nt * 32] = v;
+            done(cq, nt, acc[nt]);
           }
         }
-      };
-      if (C::S != 2) {
-        put(false);
-      } else {
-        if (k.s == 1) put(false);
-        __syncthreads();
-        if (k.s == 0) put(true);
       }
+      end(cq);
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-      __syncthreads();
-      done(cq);  // red is next written after the stage barrier of a later iteration
     }
     k.next(cq);
   }
@@ -567,101 +631,105 @@ __device__ __forceinline__ void few_stream(const FewKernel<C> &k, int item0, flo
 }
 
 template <class C>
-__device__ __forceinline__ FewKernel<C> few_kernel(const FewParams &p, const int *start,
-                                                   const uint16_t *act, const uint16_t *ent,
-                                                   uint32_t ring) {
-  const int warp = threadIdx.x >> 5;
-  const int K = C::DOWN ? p.f : p.h;
-  return FewKernel<C>{p,    start, act, ent, ring, warp, (int)(threadIdx.x & 31), warp / C::S,
-                      warp % C::S, K, (K + C::CH - 1) / C::CH,
-                      C::DOWN ? p.h / C::rows : p.f / (C::rows / 2), 0, 1, 0};
-}
-
-// Dynamic shared memory: ring | red | lists (| y sums).
-template <class C>
-struct FewSmem {
-  static constexpr int ring = C::P * C::stage, red = ring + C::red;
-};
-
-template <class C>
-__global__ void __launch_bounds__(C::threads, C::min_ctas) k_few_glu(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(C::threads, C::min_ctas)
+    k_few_glu(const __grid_constant__ FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  float *red = reinterpret_cast<float *>(smem + FewSmem<C>::ring);
-  int *start = reinterpret_cast<int *>(smem + FewSmem<C>::red);
-  uint16_t *act = reinterpret_cast<uint16_t *>(start + p.E + 1);
-  uint16_t *ent = act + min(p.E, p.T * p.k);
+  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
   __shared__ int s_act;
   pdl_wait();
   pdl_trigger();
-  const int na = few_lists<C::threads>(p, start, act, ent, &s_act);
-  FewKernel<C> k = few_kernel<C>(p, start, act, ent, smem_u32(smem));
+  const int na = few_lists<C::threads>(p, l, &s_act);
+  FewKernel<C> k(p, l, smem_u32(smem));
   k.item_end = na * k.tiles;
   k.item_step = gridDim.x;
-  few_stream(k, blockIdx.x, red, false, [&](const FewPos &q) {
-    const int nr = min(q.cnt, 8 * C::NT);
-    const int f0 = q.tile * C::outs;
-    for (int i = threadIdx.x; i < nr * C::outs; i += C::threads) {
-      const int n = i / C::outs, c = i % C::outs;
-      const float a = red_sum<C>(red, c & 7, c >> 3, n);
-      const float b = red_sum<C>(red, (c & 7) + 8, c >> 3, n);
-      const float hv = silu_f(a) * b;
-      const size_t at = (size_t)ent[q.n0 + n] * p.f + f0 + c;
-      if constexpr (C::MX4) {  // 32 lanes hold one block of 32 columns
-        static_assert(!C::MX4 || C::outs % 32 == 0, "whole blocks");
-        const int es = f16_block_exp(__reduce_max_sync(0xFFFFFFFFu, finite_abs(__float_as_uint(hv))));
-        p.hout[at] = __half_as_ushort(__float2half_rn(hv * pow2(es)));
-        if ((threadIdx.x & 31) == 0) p.hscale[at >> 5] = pow2(-es);
-      } else {
-        const __nv_bfloat16 hi = __float2bfloat16(hv);
-        const float rest = hv - __bfloat162float(hi);
-        p.hout[at] = __bfloat16_as_ushort(hi);
-        // inf - inf: the upper part already says it
-        p.hlo[at] = __bfloat16_as_ushort(__float2bfloat16(rest == rest ? rest : 0.0f));
-      }
-    }
-  });
+  float *hb = reinterpret_cast<float *>(smem + C::o_hbuf);
+  const int g = k.lane >> 2, t2 = 2 * (k.lane & 3);
+  few_stream(
+      k, blockIdx.x, reinterpret_cast<float *>(smem + C::o_red), false,
+      [&](const FewPos &q, int nt, const float (&v)[4]) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // gate v[c], up v[2 + c] of column f, token n
+          const int n = 8 * nt + t2 + c, col = k.r * 8 + g;
+          if (n >= q.cnt) continue;
+          const uint32_t en = l.ent[q.n0 + n];
+          if constexpr (C::MX4) {
+            const float xs = __ldg(p.xscale + (en >> 16));
+            hb[n * C::hrow + col] = silu_f(v[c] * xs) * (v[2 + c] * xs);
+          } else {
+            const float hv = silu_f(v[c]) * v[2 + c];
+            const size_t at = (size_t)(en & 0xFFFFu) * p.f + q.tile * C::outs + col;
+            const __nv_bfloat16 hi = __float2bfloat16(hv);
+            const float rest = hv - __bfloat162float(hi);
+            p.hout[at] = __bfloat16_as_ushort(hi);
+            // inf - inf: the upper part already says it
+            p.hlo[at] = __bfloat16_as_ushort(__float2bfloat16(rest == rest ? rest : 0.0f));
+          }
+        }
+      },
+      [&](const FewPos &q) {
+        if constexpr (C::MX4) {  // blocks of 32 columns to fp16, a warp each
+          __syncthreads();
+          const int nr = min(q.cnt, 8 * C::NT);
+          for (int i = k.warp; i < nr * (C::outs / 32); i += C::warps) {
+            const int n = i / (C::outs / 32), b = i % (C::outs / 32);
+            const float hv = hb[n * C::hrow + b * 32 + k.lane];
+            const int es =
+                f16_block_exp(__reduce_max_sync(0xFFFFFFFFu, finite_abs(__float_as_uint(hv))));
+            const size_t at =
+                (size_t)(l.ent[q.n0 + n] & 0xFFFFu) * p.f + q.tile * C::outs + b * 32 + k.lane;
+            p.hout[at] = __half_as_ushort(__float2half_rn(hv * pow2(es)));
+            if (k.lane == 0) p.hscale[at >> 5] = pow2(-es);
+          }
+        }
+      });
 }
 
-// A cluster of G CTAs shares a row tile, each with a contiguous G-th of the experts in use;
-// their sums are added in rank order through distributed shared memory.
+// A cluster of G CTAs shares a row tile, each with every G-th of the experts in use (neighbouring
+// experts of a skewed router hold similar numbers of tokens); their sums are added in rank
+// order through distributed shared memory.
 template <class C>
-__global__ void __launch_bounds__(C::threads, C::min_ctas) k_few_down(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(C::threads, C::min_ctas)
+    k_few_down(const __grid_constant__ FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  float *red = reinterpret_cast<float *>(smem + FewSmem<C>::ring);
-  int *start = reinterpret_cast<int *>(smem + FewSmem<C>::red);
-  uint16_t *act = reinterpret_cast<uint16_t *>(start + p.E + 1);
-  uint16_t *ent = act + min(p.E, p.T * p.k);
-  float *ysum = reinterpret_cast<float *>(smem + FewSmem<C>::red + few_list_bytes(p.E, p.T * p.k));
+  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
+  float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p.E, p.T * p.k));
   __shared__ int s_act;
   // Before the wait for k_few_glu: only what was complete when that kernel passed its own
   // wait (it lets this one start after that): the routing, and the caller's W2.
-  const int na = few_lists<C::threads>(p, start, act, ent, &s_act);
-  const int G = p.groups, g = (int)cluster_ctarank();
-  FewKernel<C> k = few_kernel<C>(p, start, act, ent, smem_u32(smem));
+  const int na = few_lists<C::threads>(p, l, &s_act);
+  const int G = p.groups, rank = (int)cluster_ctarank();
+  FewKernel<C> k(p, l, smem_u32(smem));
   k.fixed_tile = blockIdx.x / G;
-  const int per = (na + G - 1) / G;
-  k.item_end = min(na, (g + 1) * per);
-  for (int i = threadIdx.x; i < p.T * C::outs; i += C::threads) ysum[i] = 0.0f;
-  few_stream(k, g * per, red, true, [&](const FewPos &q) {
-    const int nr = min(q.cnt, 8 * C::NT);
-    for (int i = threadIdx.x; i < nr * C::outs; i += C::threads) {
-      const int n = i / C::outs, c = i % C::outs;
-      const int j = ent[q.n0 + n];  // an expert's entries belong to distinct tokens
-      float &y = ysum[(j / p.k) * C::outs + c];
-      y = fmaf(few_weight(p, j, q.e), red_sum<C>(red, c & 15, c >> 4, n), y);
-    }
-  });
+  k.item_end = na;
+  k.item_step = G;
+  for (int i = threadIdx.x; i < p.T * C::yrow; i += C::threads) ysum[i] = 0.0f;
+  const int g = k.lane >> 2, t2 = 2 * (k.lane & 3);
+  few_stream(
+      k, rank, reinterpret_cast<float *>(smem + C::o_red), true,
+      [&](const FewPos &q, int nt, const float (&v)[4]) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = 8 * nt + t2 + c;
+          if (n >= q.cnt) continue;
+          const uint32_t en = l.ent[q.n0 + n];  // an expert's entries belong to distinct tokens
+          const float w = few_weight(p, en & 0xFFFFu, q.e);
+          float *y = ysum + (en >> 16) * C::yrow + k.r * 16 + g;
+          y[0] = fmaf(w, v[c], y[0]);
+          y[8] = fmaf(w, v[2 + c], y[8]);
+        }
+      },
+      [](const FewPos &) {});
   cluster_sync_all();
   const int h0 = k.fixed_tile * C::outs;
   const uint32_t mine = smem_u32(ysum);
-  for (int i = g * C::threads + threadIdx.x; i < p.T * (C::outs / 2); i += G * C::threads) {
+  for (int i = rank * C::threads + threadIdx.x; i < p.T * (C::outs / 2); i += G * C::threads) {
     const int t = i / (C::outs / 2), c = 2 * (i % (C::outs / 2));
     float a = 0.0f, b = 0.0f;
     for (int o = 0; o < G; ++o) {
       float u, v;
       asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
                    : "=f"(u), "=f"(v)
-                   : "r"(mapa_shared(mine, o) + (uint32_t)((t * C::outs + c) * 4))
+                   : "r"(mapa_shared(mine, o) + (uint32_t)((t * C::yrow + c) * 4))
                    : "memory");
       a += u;
       b += v;
@@ -691,7 +759,7 @@ cudaError_t launch_few_glu(const FewParams &p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(k_few_glu<C>, done);
   if (e != cudaSuccess) return e;
-  const size_t smem = FewSmem<C>::red + few_list_bytes(p.E, p.T * p.k);
+  const size_t smem = C::o_lists + few_list_bytes(p.E, p.T * p.k);
   const long long n = (long long)p.T * p.k;
   const long long items = (n < p.E ? n : p.E) * (p.f / C::outs);
   long long ctas = device_sm_count();
@@ -704,8 +772,8 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(k_few_down<C>, done);
   if (e != cudaSuccess) return e;
-  const size_t smem = FewSmem<C>::red + few_list_bytes(p.E, p.T * p.k) +
-                      (size_t)p.T * C::outs * sizeof(float);
+  const size_t smem = C::o_lists + few_list_bytes(p.E, p.T * p.k) +
+                      (size_t)p.T * C::yrow * sizeof(float);
   const long long n = (long long)p.T * p.k;
   const int experts = (int)(n < p.E ? n : p.E);
   const int tiles = p.h / C::outs;
@@ -729,11 +797,11 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_few_down<C>, p);
 }
 
-template <bool MX4, int NT, int R, int S, int PG, int PD>
+template <bool MX4, int NT, int R, int S, int KU, int PG, int PD>
 cudaError_t launch_few_pair(const FewParams &p, const FewParams &d, cudaStream_t st) {
-  cudaError_t e = launch_few_glu<FewCfg<MX4, false, NT, R, S, PG>>(p, st);
+  cudaError_t e = launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG>>(p, st);
   if (e != cudaSuccess) return e;
-  return launch_few_down<FewCfg<MX4, true, NT, R, S, PD>>(d, st);
+  return launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD>>(d, st);
 }
 
 }  // namespace
@@ -753,16 +821,21 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   d.xin = p.hout;
   d.xlo = p.hlo;
   d.xscale = p.hscale;
+  const char *v = getenv("FEWV");
+  const int var = v ? atoi(v) : 0;
+  const double mean = (double)p.T * p.k / p.E;
+  int nt = p.T <= 8 || mean <= 3 ? 1 : p.T <= 16 || mean <= 8 ? 2 : p.T <= 32 || mean <= 20 ? 4 : 8;
+  if (var) nt = var;
   if (mx4) {
-    if (p.T <= 8) return launch_few_pair<true, 1, 4, 2, 5, 5>(p, d, st);
-    if (p.T <= 16) return launch_few_pair<true, 2, 4, 2, 4, 4>(p, d, st);
-    if (p.T <= 32) return launch_few_pair<true, 4, 8, 2, 4, 4>(p, d, st);
-    return launch_few_pair<true, 4, 8, 2, 4, 3>(p, d, st);
+    if (nt == 1) return launch_few_pair<true, 1, 4, 2, 256, 3, 3>(p, d, st);
+    if (nt == 2) return launch_few_pair<true, 2, 4, 2, 128, 4, 4>(p, d, st);
+    if (p.T <= 32) return launch_few_pair<true, 4, 8, 2, 128, 4, 4>(p, d, st);
+    return launch_few_pair<true, 4, 8, 2, 128, 4, 3>(p, d, st);
   }
-  if (p.T <= 8) return launch_few_pair<false, 1, 1, 8, 4, 3>(p, d, st);
-  if (p.T <= 16) return launch_few_pair<false, 2, 2, 4, 4, 3>(p, d, st);
-  if (p.T <= 32) return launch_few_pair<false, 4, 4, 2, 3, 3>(p, d, st);
-  return launch_few_pair<false, 8, 8, 1, 3, 3>(p, d, st);
+  if (nt == 1) return launch_few_pair<false, 1, 1, 8, 64, 4, 3>(p, d, st);
+  if (nt == 2) return launch_few_pair<false, 2, 2, 4, 64, 4, 3>(p, d, st);
+  if (nt == 4) return launch_few_pair<false, 4, 4, 2, 64, 3, 3>(p, d, st);
+  return launch_few_pair<false, 8, 8, 1, 64, 3, 3>(p, d, st);
 }
 
 }  // namespace dmoe

@@ -173,7 +173,7 @@ struct FewParams {
   const float *weights;  // [T, k]
   __nv_bfloat16 *y;      // [T, h]
   // workspace: H [T*k, f] as bf16 + bf16, or (4-bit weights) as fp16 with a scale per 32 columns,
-  // and x [T, h] in that form
+  // and x [T, h] in fp16 with a scale per row
   uint16_t *hout, *hlo, *x16;
   float *hscale, *x16scale;
   // set by launch_few for each product: its token operand, and CTAs per row tile
