@@ -190,6 +190,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with a zero accumulator going in.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -315,9 +324,11 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
   return *s_act;
 }
 
-// A place in a CTA's stream of stages: item (expert, row tile), group of 8 NT entries, chunk of K.
+// A place in a CTA's stream of stages: item (GLU: expert, row tile; DOWN: expert, part of K),
+// group of 8 NT entries, chunk of K.
 struct FewPos {
-  int item, e, tile, n0, cnt, chunk;  // cnt: entries of the expert from n0 on (may exceed 8 NT)
+  int item, e, tile, n0, cnt;  // cnt: entries of the expert from n0 on (may exceed 8 NT)
+  int chunk, c0, c1;           // chunks [c0, c1) of K
   bool on;
 };
 
@@ -328,8 +339,8 @@ struct FewKernel {
   uint32_t ring;
   int warp, lane, r, s;
   int K, chunks, tiles;
-  int item_end, item_step;  // GLU: items are (expert, tile) pairs; DOWN: experts of one tile
-  int fixed_tile;
+  int item_end, item_step;
+  int fixed_tile, part;  // DOWN: the CTA's row tile, chunks per part of K
   // this lane's rows of the tile being loaded (rows 0..7 in a, 8..15 in b), at its slice of K
   const uint8_t *wa, *wb, *ws;
 
@@ -337,24 +348,27 @@ struct FewKernel {
       : p(p_), l(l_), ring(ring_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
         r(warp / C::S), s(warp % C::S), K(C::DOWN ? p_.f : p_.h), chunks((K + C::CH - 1) / C::CH),
         tiles(C::DOWN ? p_.h / C::rows : p_.f / (C::rows / 2)), item_end(0), item_step(1),
-        fixed_tile(0), wa(nullptr), wb(nullptr), ws(nullptr) {}
+        fixed_tile(0), part(C::DOWN ? (chunks + p_.kparts - 1) / p_.kparts : 0), wa(nullptr), wb(nullptr), ws(nullptr) {}
 
   __device__ __forceinline__ void open(FewPos &q) const {
     q.on = q.item < item_end;
     if (!q.on) return;
-    const int a = C::DOWN ? q.item : q.item / tiles;
-    q.tile = C::DOWN ? fixed_tile : q.item - a * tiles;
+    const int per = C::DOWN ? p.kparts : tiles;
+    const int a = q.item / per, b = q.item - a * per;
+    q.tile = C::DOWN ? fixed_tile : b;
     q.e = l.act[a];
     q.n0 = l.start[q.e];
     q.cnt = l.start[q.e + 1] - q.n0;
-    q.chunk = 0;
+    q.c0 = C::DOWN ? b * part : 0;
+    q.c1 = C::DOWN ? min(chunks, q.c0 + part) : chunks;
+    q.chunk = q.c0;
   }
   __device__ __forceinline__ void next(FewPos &q) const {
-    if (++q.chunk < chunks) return;
+    if (++q.chunk < q.c1) return;
     if (q.cnt > 8 * C::NT) {
       q.n0 += 8 * C::NT;
       q.cnt -= 8 * C::NT;
-      q.chunk = 0;
+      q.chunk = q.c0;
       return;
     }
     q.item += item_step;
@@ -377,17 +391,17 @@ struct FewKernel {
     constexpr int row_step = 32 / seg_lanes;
     const int rr = lane / seg_lanes, seg = lane % seg_lanes;
     const size_t pitch = (size_t)K * C::wbits / 8;
-    if (q.chunk == 0) {
+    if (q.chunk == q.c0) {
       const FewWeights &fa = C::DOWN ? p.w2 : p.w1;
       const FewWeights &fb = C::DOWN ? p.w2 : p.w3;
       long long a, b;
       rows_of(q, a, b);
-      const size_t col = (size_t)s * C::KU * C::wbits / 8 + seg * 16;
+      const size_t col = (size_t)(q.c0 * C::CH + s * C::KU) * C::wbits / 8 + seg * 16;
       wa = static_cast<const uint8_t *>(fa.data) + (size_t)(a + rr) * pitch + col;
       wb = static_cast<const uint8_t *>(fb.data) + (size_t)(b + rr) * pitch + col;
       if (C::MX4 && lane < 16)  // the 16-byte piece with the row's word in it (past L1)
         ws = static_cast<const uint8_t *>(lane < 8 ? fa.scales : fb.scales) +
-             (mx4_scale_word((lane < 8 ? a : b) + (lane & 7), s * (C::KU / 128), K >> 7) &
+             (mx4_scale_word((lane < 8 ? a : b) + (lane & 7), (q.c0 * C::CH + s * C::KU) >> 7, K >> 7) &
               ~(size_t)15);
     }
     const int left = K - q.chunk * C::CH - s * C::KU;  // a multiple of 64 (4 bits: of 128)
@@ -448,6 +462,62 @@ struct FewKernel {
     }
   }
 
+  // Whether a byte of w is 0 or 255 (exact for "any": a borrow needs a zero byte below it).
+  __device__ __forceinline__ static bool odd_scales(uint32_t w) {
+    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
+  }
+
+  // Four blocks (128 columns) of this warp's 16 rows times the token tiles.
+  template <bool ODD>
+  __device__ __forceinline__ void blocks(int j, uint32_t w, uint32_t xb, uint32_t sb, uint32_t sca,
+                                         uint32_t scb, int ntl, float (&acc)[C::NT][4]) const {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int wrow = C::KU / 2;
+#pragma unroll
+    for (int b4 = 0; b4 < 4; ++b4) {
+      const int b = 4 * j + b4;
+      const uint32_t wl = w + g * wrow + (swz(g, b) << 4) + 4 * t;
+      uint32_t lo[4], hi[4];
+      mx4_unpack8(lds32(wl), lo);
+      mx4_unpack8(lds32(wl + 8 * wrow), hi);
+      float fa, fb;
+      if (ODD) {
+        fa = mx4_scale_value((sca >> (8 * b4)) & 0xFFu);
+        fb = mx4_scale_value((scb >> (8 * b4)) & 0xFFu);
+      } else {
+        fa = __uint_as_float((b4 < 3 ? sca << (23 - 8 * b4) : sca >> 1) & 0x7F800000u);
+        fb = __uint_as_float((b4 < 3 ? scb << (23 - 8 * b4) : scb >> 1) & 0x7F800000u);
+      }
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt) {
+        if (nt >= ntl) break;
+        uint32_t x0, x1, x2, x3;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                     : "r"(xb + nt * 8 * C::x_row + b * 64)
+                     : "memory");
+        float c[4];
+        mma_f16_zero(c, lo[0], hi[0], lo[1], hi[1], x0, x1);
+        mma_f16(c, lo[2], hi[2], lo[3], hi[3], x2, x3);
+        if constexpr (C::SB) {
+          float s0, s1;
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(s0), "=f"(s1)
+                       : "r"(sb + (b * 8 * C::NT + nt * 8) * 4)
+                       : "memory");
+          c[0] *= s0;
+          c[1] *= s1;
+          c[2] *= s0;
+          c[3] *= s1;
+        }
+        acc[nt][0] = fmaf(c[0], fa, acc[nt][0]);
+        acc[nt][1] = fmaf(c[1], fa, acc[nt][1]);
+        acc[nt][2] = fmaf(c[2], fb, acc[nt][2]);
+        acc[nt][3] = fmaf(c[3], fb, acc[nt][3]);
+      }
+    }
+  }
+
   __device__ __forceinline__ void multiply(const FewPos &q, int st, float (&acc)[C::NT][4]) const {
     const int left = K - q.chunk * C::CH - s * C::KU;
     if (left <= 0) return;
@@ -461,48 +531,15 @@ struct FewKernel {
       const uint32_t sw = base + C::o_sc + warp * C::sc_warp + g * 16 + ((ra >> 5) & 3) * 4;
       const uint32_t xb = base + C::o_x + g * C::x_row + (s * C::KU + 8 * t) * 2;
       const uint32_t sb = base + C::o_sb + (s * (C::KU / 32) * 8 * C::NT + 2 * t) * 4;
-      constexpr int wrow = C::KU / 2;
 #pragma unroll
       for (int j = 0; j < C::KU / 128; ++j) {
         if (j * 128 >= left) break;
         const uint32_t sca = lds32(sw + 256 * j), scb = lds32(sw + 256 * j + 128);
-#pragma unroll
-        for (int b4 = 0; b4 < 4; ++b4) {
-          const int b = 4 * j + b4;
-          const uint32_t wl = w + g * wrow + (swz(g, b) << 4) + 4 * t;
-          uint32_t lo[4], hi[4];
-          mx4_unpack8(lds32(wl), lo);
-          mx4_unpack8(lds32(wl + 8 * wrow), hi);
-          const float fa = mx4_scale_value((sca >> (8 * b4)) & 0xFFu);
-          const float fb = mx4_scale_value((scb >> (8 * b4)) & 0xFFu);
-#pragma unroll
-          for (int nt = 0; nt < C::NT; ++nt) {
-            if (nt >= ntl) break;
-            uint32_t x0, x1, x2, x3;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                         : "r"(xb + nt * 8 * C::x_row + b * 64)
-                         : "memory");
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(c, lo[0], hi[0], lo[1], hi[1], x0, x1);
-            mma_f16(c, lo[2], hi[2], lo[3], hi[3], x2, x3);
-            if constexpr (C::SB) {
-              float s0, s1;
-              asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                           : "=f"(s0), "=f"(s1)
-                           : "r"(sb + (b * 8 * C::NT + nt * 8) * 4)
-                           : "memory");
-              c[0] *= s0;
-              c[1] *= s1;
-              c[2] *= s0;
-              c[3] *= s1;
-            }
-            acc[nt][0] = fmaf(c[0], fa, acc[nt][0]);
-            acc[nt][1] = fmaf(c[1], fa, acc[nt][1]);
-            acc[nt][2] = fmaf(c[2], fb, acc[nt][2]);
-            acc[nt][3] = fmaf(c[3], fb, acc[nt][3]);
-          }
-        }
+        // scale bytes 1 .. 254 are exponent fields as they stand; 0 (2^-127) and 255 (NaN) are not
+        if (__any_sync(0xFFFFFFFFu, odd_scales(sca) | odd_scales(scb)))
+          blocks<true>(j, w, xb, sb, sca, scb, ntl, acc);
+        else
+          blocks<false>(j, w, xb, sb, sca, scb, ntl, acc);
       }
     } else {
       const int ar = lane & 15;
@@ -588,7 +625,7 @@ __device__ __forceinline__ void few_stream(FewKernel<C> &k, int item0, float *re
     if (++ld == C::P) ld = 0;
     k.multiply(cq, st, acc);
     if (++st == C::P) st = 0;
-    if (cq.chunk == k.chunks - 1) {
+    if (cq.chunk == cq.c1 - 1) {
       const int ntl = (min(cq.cnt, 8 * C::NT) + 7) >> 3;
       // slices past the first hand over their sums (red is next written after the stage
       // barrier of a later iteration)
@@ -700,7 +737,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   const int G = p.groups, rank = (int)cluster_ctarank();
   FewKernel<C> k(p, l, smem_u32(smem));
   k.fixed_tile = blockIdx.x / G;
-  k.item_end = na;
+  k.item_end = na * p.kparts;
   k.item_step = G;
   for (int i = threadIdx.x; i < p.T * C::yrow; i += C::threads) ysum[i] = 0.0f;
   const int g = k.lane >> 2, t2 = 2 * (k.lane & 3);
@@ -777,9 +814,18 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   const long long n = (long long)p.T * p.k;
   const int experts = (int)(n < p.E ? n : p.E);
   const int tiles = p.h / C::outs;
-  // experts split over up to eight CTAs per row tile until the SMs are covered
+  // the experts are spread over up to eight CTAs per row tile until there is one CTA for each
+  // place on the SMs; with fewer experts than that, K is cut into parts as well (whole chunks)
+  int places = device_sm_count();
+  if (2 * (smem + 2048) <= 228 * 1024 && C::min_ctas > 1) places *= 2;
   int G = 1;
-  while (G < 8 && 2 * G <= experts && tiles * G < device_sm_count()) G *= 2;
+  while (G < 8 && tiles * G * 2 <= places) G *= 2;
+  const int chunks = (p.f + C::CH - 1) / C::CH;
+  int parts = 1;
+  while (experts * parts < G && parts * 2 <= chunks) parts *= 2;
+  const int part = (chunks + parts - 1) / parts;
+  p.kparts = (chunks + part - 1) / part;  // no empty part
+  while (G > 1 && experts * p.kparts < G) G /= 2;
   p.groups = G;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * G);

@@ -176,10 +176,10 @@ struct FewParams {
   // and x [T, h] in fp16 with a scale per row
   uint16_t *hout, *hlo, *x16;
   float *hscale, *x16scale;
-  // set by launch_few for each product: its token operand, and CTAs per row tile
+  // set by launch_few for each product: its token operand; DOWN: CTAs per row tile, parts of K
   const uint16_t *xin, *xlo;
   const float *xscale;
-  int groups;
+  int groups, kparts;
 };
 // logits given: top and weights are written first; else they are inputs.
 cudaError_t launch_few(const FewParams &p, const uint16_t *logits, bool renorm, int32_t *top,
