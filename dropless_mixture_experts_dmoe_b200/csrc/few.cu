@@ -7,14 +7,15 @@
 // nothing is padded, x and H are read from L2, and every kernel is a stream of weight tiles.
 //
 // A CTA multiplies tiles of 16 R weight rows (8 R gate and 8 R up rows in k_few_glu) by the
-// columns of up to 8 NT of the expert's tokens.  Its warps are R row tiles x S slices of K; a
-// stage of the ring holds each warp's 16 rows x KU columns, fetched by the warp itself with
-// 16-byte cp.async (a lane group per 128-byte line), and the tokens' S * KU columns.  The
-// products run on mma.sync m16n8k16 with the weights as the 16-row operand: a tile of 16 rows
-// costs one instruction per 16 K and 8 tokens, far below the tensor rate at these sizes; what
-// counts is that 40 KB and more per SM are in flight at all times, so the ring runs on from one
-// tile into the next, across experts.  tcgen05 would need 128-row tiles and a full shared-memory
-// operand for 1 to 8 columns, and the 4-bit weights converted into it.
+// columns of up to 8 NT of the expert's tokens.  Its warps are R row tiles x S slices of K, and
+// one more that fills a ring of stages: TMA boxes of the weight rows (swizzled), bulk copies of
+// the tokens' rows and of the scales.  The products run on mma.sync m16n8k16 with the weights
+// as the 16-row operand: a tile of 16 rows costs one instruction per 16 K and 8 tokens, far
+// below the tensor rate at these sizes; what counts is that 80 KB and more per SM are in flight
+// at all times, so the ring runs on from one tile into the next, across experts, and that the
+// multiplying warps spend few instructions on anything but the products.  tcgen05 would need
+// 128-row tiles and a full shared-memory operand for 1 to 8 columns, and the 4-bit weights
+// converted into it.
 //   bf16 weights: x as bf16; H as the sum of two bf16 (16 bits), multiplied in turn.
 //   4-bit weights: e2m1 -> fp16 is exact, so x and H go in fp16 under a power-of-two scale, x per
 //     row (exact down to 2^-29 of the row's largest), H per 32 columns (11 bits); the 32
@@ -160,16 +161,27 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 
 // ---- the product kernels -----------------------------------------------------------------------
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copy `bytes` (a multiple of 16, both addresses too) to this CTA's shared memory, counted on bar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(
+                   smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -182,10 +194,24 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t a) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -199,47 +225,44 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Shape of a variant: MX4 weights in four bits; DOWN the second product; NT tiles of 8 tokens;
-// R x S warps of KU columns; P stages.  BR: copies of the token rows (two: H's upper and lower
-// bf16).  SB: the token operand has a scale per 32 columns (H in fp16).
+// R x S multiplying warps of KU columns; P stages.  BR: copies of the token rows (two: H's
+// upper and lower bf16).  SB: the token operand has a scale per 32 columns (H in fp16).
 template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int KU_, int P_>
 struct FewCfg {
   static constexpr bool MX4 = MX4_, DOWN = DOWN_, SB = MX4 && DOWN;
   static constexpr int NT = NT_, R = R_, S = S_, KU = KU_, P = P_;
-  static constexpr int warps = R * S, threads = 32 * warps;
-  static constexpr int min_ctas = threads == 256 ? 2 : 1;
+  static constexpr int warps = R * S, threads = 32 * warps + 32;
+  static constexpr int min_ctas = warps == 8 ? 2 : 1;
   static constexpr int CH = S * KU;  // columns per stage
   static constexpr int BR = (DOWN && !MX4) ? 2 : 1;
-  static constexpr int wbits = MX4 ? 4 : 16;
-  static constexpr int w_warp = 16 * KU * wbits / 8;       // weight bytes per warp and stage
-  static constexpr int sc_warp = MX4 ? KU / 128 * 256 : 0;  // scales: 16 bytes per row and 128 K
+  // weights: [W1, W3 | W2][slices of SC columns][rows][row_b bytes], as TMA boxes land
+  static constexpr int SC = MX4 ? 128 : 64, slices = CH / SC;
+  static constexpr int row_b = MX4 ? 64 : 128;
+  static constexpr int mats = DOWN ? 1 : 2, rows_m = DOWN ? 16 * R : 8 * R;
+  static constexpr int w_mat = slices * rows_m * row_b, w_bytes = mats * w_mat;
+  static constexpr int sc_mat = MX4 ? CH / 128 * kMx4TileBytes : 0;  // whole scale tiles
   // token rows: a stride that is 16 (ldmatrix) or 64 (16-byte loads of 4 lanes a row) bytes off
   // a multiple of 128 keeps the reads free of bank conflicts
   static constexpr int x_row = CH * 2 + (MX4 ? 64 : 16);
   static constexpr int x_bytes = BR * 8 * NT * x_row;
-  static constexpr int sb_bytes = SB ? (CH / 32) * 8 * NT * 4 : 0;  // token scales [block][token]
-  static constexpr int o_sc = warps * w_warp, o_x = o_sc + warps * sc_warp, o_sb = o_x + x_bytes;
-  static constexpr int stage = o_sb + sb_bytes;
-  static constexpr int rows = 16 * R;                  // weight rows per tile
-  static constexpr int outs = DOWN ? rows : rows / 2;  // output columns per tile
-  // partial sums: of the slices of K past the first, and for GLU MX4 a tile's H in fp32
+  static constexpr int sb_row = CH / 8 + 16;  // a token's block scales
+  static constexpr int sb_bytes = SB ? 8 * NT * sb_row : 0;
+  static constexpr int o_sc = w_bytes, o_x = o_sc + mats * sc_mat, o_sb = o_x + x_bytes;
+  static constexpr int stage = (o_sb + sb_bytes + 1023) / 1024 * 1024;
+  static constexpr int outs = DOWN ? 16 * R : 8 * R;  // output columns per tile
+  // partial sums of the slices of K past the first, and for GLU MX4 a tile's H in fp32
   static constexpr int red = (S - 1) * R * NT * 512;
   static constexpr int hrow = outs + 4;
   static constexpr int hbuf = (MX4 && !DOWN) ? 8 * NT * hrow * 4 : 0;
   // y sums: rows of `outs` plus 8 floats (four tokens x eight rows meet no bank twice)
-  static constexpr int yrow = outs + 8;
-  static constexpr int o_red = P * stage, o_hbuf = o_red + red, o_lists = o_hbuf + hbuf;
-  static_assert(stage % 16 == 0 && o_x % 16 == 0 && x_row % 16 == 0, "alignment");
-  static_assert(!MX4 || DOWN || outs % 32 == 0, "whole blocks of H");
+  static constexpr int yrow = DOWN ? outs + 8 : 0, y_row_bytes = yrow * 4;
+  static constexpr int o_red = P * stage, o_hbuf = o_red + red, o_bars = o_hbuf + hbuf,
+                       o_lists = o_bars + 128;
+  static constexpr int fixed = 1024 + o_lists;  // the ring starts on a 1024-byte boundary
+  static_assert(w_mat % 1024 == 0 && (!MX4 || DOWN || outs % 32 == 0), "boxes, whole blocks of H");
+  static_assert(2 * P * 8 <= 112, "barriers");
 };
 
 // Bytes of the expert lists: entries [n] (j | token << 16), starts [E + 1], experts in use
@@ -327,8 +350,9 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
 // A place in a CTA's stream of stages: item (GLU: expert, row tile; DOWN: expert, part of K),
 // group of 8 NT entries, chunk of K.
 struct FewPos {
-  int item, e, tile, n0, cnt;  // cnt: entries of the expert from n0 on (may exceed 8 NT)
-  int chunk, c0, c1;           // chunks [c0, c1) of K
+  int a, b;             // index of the expert in use; tile or part
+  int e, n0, cnt;       // cnt: entries of the expert from n0 on (may exceed 8 NT)
+  int chunk, c0, c1;    // chunks [c0, c1) of K
   bool on;
 };
 
@@ -337,31 +361,33 @@ struct FewKernel {
   const FewParams &p;
   const FewLists &l;
   uint32_t ring;
-  int warp, lane, r, s;
-  int K, chunks, tiles;
-  int item_end, item_step;
-  int fixed_tile, part;  // DOWN: the CTA's row tile, chunks per part of K
-  // this lane's rows of the tile being loaded (rows 0..7 in a, 8..15 in b), at its slice of K
-  const uint8_t *wa, *wb, *ws;
-
-  __device__ __forceinline__ FewKernel(const FewParams &p_, const FewLists &l_, uint32_t ring_)
-      : p(p_), l(l_), ring(ring_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
-        r(warp / C::S), s(warp % C::S), K(C::DOWN ? p_.f : p_.h), chunks((K + C::CH - 1) / C::CH),
-        tiles(C::DOWN ? p_.h / C::rows : p_.f / (C::rows / 2)), item_end(0), item_step(1),
-        fixed_tile(0), part(C::DOWN ? (chunks + p_.kparts - 1) / p_.kparts : 0), wa(nullptr), wb(nullptr), ws(nullptr) {}
+  uint64_t *full, *empty;
+  volatile int *abort_flag;
+  int K, chunks, na;
+  int per, step;         // items per expert; items from one of this CTA's to its next
+  int tile, part;        // DOWN: the CTA's row tile, chunks per part of K
 
   __device__ __forceinline__ void open(FewPos &q) const {
-    q.on = q.item < item_end;
+    if (q.b >= per) {
+      const int d = q.b / per;
+      q.a += d;
+      q.b -= d * per;
+    }
+    q.on = q.a < na;
     if (!q.on) return;
-    const int per = C::DOWN ? p.kparts : tiles;
-    const int a = q.item / per, b = q.item - a * per;
-    q.tile = C::DOWN ? fixed_tile : b;
-    q.e = l.act[a];
+    q.e = l.act[q.a];
     q.n0 = l.start[q.e];
     q.cnt = l.start[q.e + 1] - q.n0;
-    q.c0 = C::DOWN ? b * part : 0;
+    q.c0 = C::DOWN ? q.b * part : 0;
     q.c1 = C::DOWN ? min(chunks, q.c0 + part) : chunks;
     q.chunk = q.c0;
+  }
+  __device__ __forceinline__ FewPos first(int item) const {
+    FewPos q;
+    q.a = 0;
+    q.b = item;
+    open(q);
+    return q;
   }
   __device__ __forceinline__ void next(FewPos &q) const {
     if (++q.chunk < q.c1) return;
@@ -371,144 +397,145 @@ struct FewKernel {
       q.chunk = q.c0;
       return;
     }
-    q.item += item_step;
+    q.b += step;
     open(q);
   }
+  __device__ __forceinline__ int tile_of(const FewPos &q) const { return C::DOWN ? tile : q.b; }
 
-  // Row 0 (a) and row 8 (b) of this warp's 16 in the tile.
-  __device__ __forceinline__ void rows_of(const FewPos &q, long long &a, long long &b) const {
-    if (C::DOWN) {
-      a = (long long)q.e * p.h + q.tile * C::rows + r * 16;
-      b = a + 8;
-    } else {
-      a = b = (long long)q.e * p.f + q.tile * (C::rows / 2) + r * 8;
+  // ---- the loading warp ----
+
+  // Columns of K in the stage, and the bytes that its copies bring.
+  __device__ __forceinline__ int width(const FewPos &q) const {
+    return min(C::CH, K - q.chunk * C::CH);
+  }
+  __device__ __forceinline__ uint32_t bytes(const FewPos &q) const {
+    const uint32_t w = width(q), nr = min(q.cnt, 8 * C::NT);
+    return C::w_bytes + (C::MX4 ? C::mats * (w >> 7) * kMx4TileBytes : 0) +
+           nr * (C::BR * w * 2 + (C::SB ? w >> 3 : 0));
+  }
+  // Weights and their scales (one lane).
+  __device__ __forceinline__ void load_w(const FewPos &q, int st) const {
+    const uint32_t dst = ring + st * C::stage, bar = smem_u32(&full[st]);
+    const int row = C::DOWN ? q.e * p.h + tile * C::outs : q.e * p.f + q.b * C::outs;
+    tma_load_3d(dst, &p.tw[0], bar, 0, row, q.chunk * C::slices);
+    if (!C::DOWN) tma_load_3d(dst + C::w_mat, &p.tw[1], bar, 0, row, q.chunk * C::slices);
+    if (C::MX4) {
+      const uint32_t n = (width(q) >> 7) * kMx4TileBytes;
+      const size_t at = ((size_t)(row >> 7) * (K >> 7) + q.chunk * (C::CH / 128)) * kMx4TileBytes;
+      bulk_load(dst + C::o_sc, p.ws[0] + at, n, bar);
+      if (!C::DOWN) bulk_load(dst + C::o_sc + C::sc_mat, p.ws[1] + at, n, bar);
     }
   }
-
-  // This warp's 16 weight rows of the stage.
-  __device__ __forceinline__ void load_w(const FewPos &q, int st) {
-    constexpr int seg_lanes = C::MX4 ? C::KU / 32 : 8;  // lanes (16 bytes each) per row
-    constexpr int row_step = 32 / seg_lanes;
-    const int rr = lane / seg_lanes, seg = lane % seg_lanes;
-    const size_t pitch = (size_t)K * C::wbits / 8;
-    if (q.chunk == q.c0) {
-      const FewWeights &fa = C::DOWN ? p.w2 : p.w1;
-      const FewWeights &fb = C::DOWN ? p.w2 : p.w3;
-      long long a, b;
-      rows_of(q, a, b);
-      const size_t col = (size_t)(q.c0 * C::CH + s * C::KU) * C::wbits / 8 + seg * 16;
-      wa = static_cast<const uint8_t *>(fa.data) + (size_t)(a + rr) * pitch + col;
-      wb = static_cast<const uint8_t *>(fb.data) + (size_t)(b + rr) * pitch + col;
-      if (C::MX4 && lane < 16)  // the 16-byte piece with the row's word in it (past L1)
-        ws = static_cast<const uint8_t *>(lane < 8 ? fa.scales : fb.scales) +
-             (mx4_scale_word((lane < 8 ? a : b) + (lane & 7), (q.c0 * C::CH + s * C::KU) >> 7, K >> 7) &
-              ~(size_t)15);
-    }
-    const int left = K - q.chunk * C::CH - s * C::KU;  // a multiple of 64 (4 bits: of 128)
-    if (left > 0) {
-      const uint32_t dst = ring + st * C::stage + warp * C::w_warp;
-      if (seg * (C::MX4 ? 32 : 8) < left) {
-#pragma unroll
-        for (int i = 0; i < 8; i += row_step) {
-          const int row = i + rr;
-          const uint32_t d = dst + row * (seg_lanes * 16) + (swz(row, seg) << 4);
-          cp16(d, wa + i * pitch);
-          cp16(d + 8 * seg_lanes * 16, wb + i * pitch);
-        }
-      }
-      if (C::MX4 && lane < 16) {
-        const uint32_t d = ring + st * C::stage + C::o_sc + warp * C::sc_warp + lane * 16;
-#pragma unroll
-        for (int j = 0; j < C::KU / 128; ++j)
-          if (j * 128 < left) cp16(d + 256 * j, ws + kMx4TileBytes * j);
-      }
-    }
-    wa += C::CH * C::wbits / 8;
-    wb += C::CH * C::wbits / 8;
-    ws += (C::CH / 128) * kMx4TileBytes;
-  }
-
-  // Place of 16-byte piece `seg` of a weight row in its row of the stage.  bf16: ldmatrix reads
-  // one piece of eight rows.  4 bits: eight rows' four words of a piece (32 lanes) are read; rows
-  // of 64 bytes share their banks with every second row, rows of 128 bytes with every row.
-  __device__ __forceinline__ static int swz(int row, int seg) {
-    if (!C::MX4) return seg ^ (row & 7);
-    return C::KU == 128 ? seg ^ ((row >> 1) & 3) : seg ^ (row & 7);
-  }
-
-  // The token rows of the stage (columns past K are not loaded and not used).
-  __device__ __forceinline__ void load_x(const FewPos &q, int st) const {
-    constexpr int segs = C::CH / 8;  // 16-byte pieces per row
+  // Token rows (all lanes).
+  __device__ __forceinline__ void load_x(const FewPos &q, int st, int lane) const {
+    const uint32_t dst = ring + st * C::stage, bar = smem_u32(&full[st]);
     const int nr = min(q.cnt, 8 * C::NT);
-    const int c0 = q.chunk * C::CH;
-    const uint32_t dst = ring + st * C::stage + C::o_x;
-    for (int i = threadIdx.x; i < nr * segs; i += C::threads) {
-      const int n = i / segs, seg = i % segs;
-      if (c0 + seg * 8 >= K) continue;
+    const uint32_t w = width(q);
+    for (int n = lane; n < nr; n += 32) {
       const uint32_t v = l.ent[q.n0 + n];
-      const size_t at = (size_t)(C::DOWN ? v & 0xFFFFu : v >> 16) * K + c0 + seg * 8;
-      cp16(dst + n * C::x_row + seg * 16, p.xin + at);
-      if (C::BR == 2) cp16(dst + (8 * C::NT + n) * C::x_row + seg * 16, p.xlo + at);
-    }
-    if constexpr (C::SB) {
-      constexpr int nb = C::CH / 32;
-      for (int i = threadIdx.x; i < nr * nb; i += C::threads) {
-        const int n = i / nb, b = i % nb;
-        if (c0 + b * 32 >= K) continue;
-        const size_t row = l.ent[q.n0 + n] & 0xFFFFu;
-        cp4(ring + st * C::stage + C::o_sb + (b * 8 * C::NT + n) * 4,
-            p.xscale + row * (K >> 5) + (c0 >> 5) + b);
-      }
+      const size_t row = C::DOWN ? v & 0xFFFFu : v >> 16;
+      const size_t at = row * K + q.chunk * C::CH;
+      bulk_load(dst + C::o_x + n * C::x_row, p.xin + at, w * 2, bar);
+      if (C::BR == 2) bulk_load(dst + C::o_x + (8 * C::NT + n) * C::x_row, p.xlo + at, w * 2, bar);
+      if (C::SB) bulk_load(dst + C::o_sb + n * C::sb_row, p.xscale + (at >> 5), w >> 3, bar);
     }
   }
+
+  // pre: the weights of the first stages are loaded before the wait for the earlier kernels.
+  __device__ __forceinline__ void produce(int item0, bool pre, int lane) const {
+    FewPos q = first(item0), w = q;
+    if (pre) {
+      for (int st = 0; st < C::P && w.on; ++st) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[st], bytes(w));
+          load_w(w, st);
+        }
+        next(w);
+      }
+      pdl_wait();
+    }
+    int st = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    while (q.on) {
+      if (issued >= C::P) {
+        int good = 1;
+        if (lane == 0) good = mbar_wait(&empty[st], phase ^ 1u, p.status, abort_flag) ? 1 : 0;
+        if (!__shfl_sync(0xFFFFFFFFu, good, 0)) break;
+      }
+      if (lane == 0 && !(pre && issued < C::P)) {
+        mbar_arrive_expect_tx(&full[st], bytes(q));
+        load_w(q, st);
+      }
+      __syncwarp();  // the expected bytes are set before any of them can arrive
+      load_x(q, st, lane);
+      ++issued;
+      next(q);
+      if (++st == C::P) {
+        st = 0;
+        phase ^= 1u;
+      }
+    }
+    if (lane == 0)  // every copy has landed before the CTA's memory is given up
+      for (long long i = (issued > C::P ? issued - C::P : 0); i < issued; ++i)
+        mbar_wait_plain(&full[i % C::P], (uint32_t)((i / C::P) & 1));
+  }
+
+  // ---- the multiplying warps ----
 
   // Whether a byte of w is 0 or 255 (exact for "any": a borrow needs a zero byte below it).
   __device__ __forceinline__ static bool odd_scales(uint32_t w) {
     return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
   }
 
-  // Four blocks (128 columns) of this warp's 16 rows times the token tiles.
+  // Four blocks (128 columns, a slice) of a warp's 16 rows times the token tiles.  wl: this
+  // lane's word of row lane / 4 in the slice; xb, sb: its token row and the token scales.
   template <bool ODD>
-  __device__ __forceinline__ void blocks(int j, uint32_t w, uint32_t xb, uint32_t sb, uint32_t sca,
+  __device__ __forceinline__ void blocks(uint32_t wl, uint32_t xb, uint32_t sb, uint32_t sca,
                                          uint32_t scb, int ntl, float (&acc)[C::NT][4]) const {
-    const int g = lane >> 2, t = lane & 3;
-    constexpr int wrow = C::KU / 2;
+    constexpr int up = C::DOWN ? 8 * C::row_b : C::w_mat;  // from row i to row i + 8
+    constexpr bool ahead = C::SB && C::NT <= 2;  // a slice's token scales fit in registers
+    uint32_t s0[C::NT][4], s1[C::NT][4];
+    if constexpr (ahead) {
 #pragma unroll
-    for (int b4 = 0; b4 < 4; ++b4) {
-      const int b = 4 * j + b4;
-      const uint32_t wl = w + g * wrow + (swz(g, b) << 4) + 4 * t;
+      for (int nt = 0; nt < C::NT; ++nt) {
+        if (nt >= ntl) break;
+        lds128(s0[nt], sb + nt * 8 * C::sb_row);
+        lds128(s1[nt], sb + (nt * 8 + 1) * C::sb_row);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t wa = wl ^ (b << 4);
       uint32_t lo[4], hi[4];
-      mx4_unpack8(lds32(wl), lo);
-      mx4_unpack8(lds32(wl + 8 * wrow), hi);
+      mx4_unpack8(lds32(wa), lo);
+      mx4_unpack8(lds32(wa + up), hi);
       float fa, fb;
       if (ODD) {
-        fa = mx4_scale_value((sca >> (8 * b4)) & 0xFFu);
-        fb = mx4_scale_value((scb >> (8 * b4)) & 0xFFu);
+        fa = mx4_scale_value((sca >> (8 * b)) & 0xFFu);
+        fb = mx4_scale_value((scb >> (8 * b)) & 0xFFu);
       } else {
-        fa = __uint_as_float((b4 < 3 ? sca << (23 - 8 * b4) : sca >> 1) & 0x7F800000u);
-        fb = __uint_as_float((b4 < 3 ? scb << (23 - 8 * b4) : scb >> 1) & 0x7F800000u);
+        fa = __uint_as_float((b < 3 ? sca << (23 - 8 * b) : sca >> 1) & 0x7F800000u);
+        fb = __uint_as_float((b < 3 ? scb << (23 - 8 * b) : scb >> 1) & 0x7F800000u);
       }
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
         if (nt >= ntl) break;
-        uint32_t x0, x1, x2, x3;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                     : "r"(xb + nt * 8 * C::x_row + b * 64)
-                     : "memory");
+        uint32_t x[4];
+        lds128(x, xb + nt * 8 * C::x_row + b * 64);
         float c[4];
-        mma_f16_zero(c, lo[0], hi[0], lo[1], hi[1], x0, x1);
-        mma_f16(c, lo[2], hi[2], lo[3], hi[3], x2, x3);
+        mma_f16_zero(c, lo[0], hi[0], lo[1], hi[1], x[0], x[1]);
+        mma_f16(c, lo[2], hi[2], lo[3], hi[3], x[2], x[3]);
         if constexpr (C::SB) {
-          float s0, s1;
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                       : "=f"(s0), "=f"(s1)
-                       : "r"(sb + (b * 8 * C::NT + nt * 8) * 4)
-                       : "memory");
-          c[0] *= s0;
-          c[1] *= s1;
-          c[2] *= s0;
-          c[3] *= s1;
+          if constexpr (!ahead) {
+            s0[nt][b] = lds32(sb + nt * 8 * C::sb_row + 4 * b);
+            s1[nt][b] = lds32(sb + (nt * 8 + 1) * C::sb_row + 4 * b);
+          }
+          const float u = __uint_as_float(s0[nt][b]), v = __uint_as_float(s1[nt][b]);
+          c[0] *= u;
+          c[1] *= v;
+          c[2] *= u;
+          c[3] *= v;
         }
         acc[nt][0] = fmaf(c[0], fa, acc[nt][0]);
         acc[nt][1] = fmaf(c[1], fa, acc[nt][1]);
@@ -518,37 +545,46 @@ struct FewKernel {
     }
   }
 
-  __device__ __forceinline__ void multiply(const FewPos &q, int st, float (&acc)[C::NT][4]) const {
+  __device__ __forceinline__ void multiply(const FewPos &q, int st, int r, int s, int lane,
+                                           float (&acc)[C::NT][4]) const {
     const int left = K - q.chunk * C::CH - s * C::KU;
     if (left <= 0) return;
     const uint32_t base = ring + st * C::stage;
-    const uint32_t w = base + warp * C::w_warp;
     const int ntl = (min(q.cnt, 8 * C::NT) + 7) >> 3;
     if constexpr (C::MX4) {
       const int g = lane >> 2, t = lane & 3;
-      // rows 0..7 and 8..15 of a tile start at multiples of 8: one 32-row group each
-      const int ra = q.tile * C::outs + r * (C::DOWN ? 16 : 8);
-      const uint32_t sw = base + C::o_sc + warp * C::sc_warp + g * 16 + ((ra >> 5) & 3) * 4;
+      const int row = r * (C::DOWN ? 16 : 8) + g;  // of the box
+      const uint32_t w = base + s * (C::KU / 128) * C::rows_m * 64 + row * 64 +
+                         (((row >> 1) & 3) << 4) + 4 * t;
+      // the tile's rows start at a multiple of 8: rows 0..7 and 8..15 stay in one 32-row group
+      const int r128 = (tile_of(q) * C::outs + row) & 127;
+      const uint32_t sw = base + C::o_sc + s * (C::KU / 128) * kMx4TileBytes + (r128 & 31) * 16 +
+                          (r128 >> 5) * 4;
+      constexpr int sup = C::DOWN ? 128 : C::sc_mat;
       const uint32_t xb = base + C::o_x + g * C::x_row + (s * C::KU + 8 * t) * 2;
-      const uint32_t sb = base + C::o_sb + (s * (C::KU / 32) * 8 * C::NT + 2 * t) * 4;
+      const uint32_t sb = base + C::o_sb + 2 * t * C::sb_row + s * (C::KU / 8);
 #pragma unroll
       for (int j = 0; j < C::KU / 128; ++j) {
         if (j * 128 >= left) break;
-        const uint32_t sca = lds32(sw + 256 * j), scb = lds32(sw + 256 * j + 128);
+        const uint32_t sca = lds32(sw + j * kMx4TileBytes);
+        const uint32_t scb = lds32(sw + j * kMx4TileBytes + sup);
         // scale bytes 1 .. 254 are exponent fields as they stand; 0 (2^-127) and 255 (NaN) are not
         if (__any_sync(0xFFFFFFFFu, odd_scales(sca) | odd_scales(scb)))
-          blocks<true>(j, w, xb, sb, sca, scb, ntl, acc);
+          blocks<true>(w + j * C::rows_m * 64, xb + j * 256, sb + j * 16, sca, scb, ntl, acc);
         else
-          blocks<false>(j, w, xb, sb, sca, scb, ntl, acc);
+          blocks<false>(w + j * C::rows_m * 64, xb + j * 256, sb + j * 16, sca, scb, ntl, acc);
       }
     } else {
       const int ar = lane & 15;
+      const uint32_t wr = base + s * C::rows_m * 128 +
+                          (C::DOWN ? (r * 16 + ar) * 128
+                                   : (ar >> 3) * C::w_mat + (r * 8 + (ar & 7)) * 128);
       const uint32_t xb = base + C::o_x + (lane & 7) * C::x_row + (s * C::KU + (lane >> 3) * 8) * 2;
 #pragma unroll
       for (int kk = 0; kk < 4; kk += 2) {
         uint32_t a0[4], a1[4];
-        ldsm4(a0, w + ar * 128 + (swz(ar, 2 * kk + (lane >> 4)) << 4));
-        ldsm4(a1, w + ar * 128 + (swz(ar, 2 * kk + 2 + (lane >> 4)) << 4));
+        ldsm4(a0, wr + (((2 * kk + (lane >> 4)) ^ (ar & 7)) << 4));
+        ldsm4(a1, wr + (((2 * kk + 2 + (lane >> 4)) ^ (ar & 7)) << 4));
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
           if (nt >= ntl) break;
@@ -556,137 +592,129 @@ struct FewKernel {
           for (int br = 0; br < C::BR; ++br) {
             uint32_t x[4];
             ldsm4(x, xb + (br * 8 * C::NT + nt * 8) * C::x_row + kk * 32);
-            mma_bf16(acc[nt], a0[0], a0[1], a0[2], a0[3], x[0], x[1]);
-            mma_bf16(acc[nt], a1[0], a1[1], a1[2], a1[3], x[2], x[3]);
+            mma_bf16(acc[nt], a0, x[0], x[1]);
+            mma_bf16(acc[nt], a1, x[2], x[3]);
           }
         }
       }
     }
   }
-};
 
-// The stream of stages that both products share.  pre: before the wait for the earlier kernels
-// only weights are loaded.  done(pos, nt, sums): called by the first slice's warps with the
-// sums of token tile nt over all of K: words 2 i + c are row lane / 4 + 8 i of the warp's 16 and
-// token 8 nt + 2 (lane % 4) + c; end(pos): by all threads after them.
-template <class C, class Done, class End>
-__device__ __forceinline__ void few_stream(FewKernel<C> &k, int item0, float *red, bool pre,
-                                           Done done, End end) {
-  FewPos pq;  // what is loaded next
-  pq.item = item0;
-  k.open(pq);
-  FewPos cq = pq;
-  if (pre) {  // weights of the first stages now, their token rows once the earlier kernel is done
-    FewPos xq = pq;
-#pragma unroll
-    for (int i = 0; i < C::P - 1; ++i) {
-      if (pq.on) {
-        k.load_w(pq, i);
-        k.next(pq);
-      }
-      cp_commit();
-    }
-    pdl_wait();
-    pdl_trigger();
-#pragma unroll
-    for (int i = 0; i < C::P - 1; ++i) {
-      if (xq.on) {
-        k.load_x(xq, i);
-        k.next(xq);
-      }
-      cp_commit();
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < C::P - 1; ++i) {
-      if (pq.on) {
-        k.load_w(pq, i);
-        k.load_x(pq, i);
-        k.next(pq);
-      }
-      cp_commit();
-    }
+  // Among the multiplying warps.
+  __device__ __forceinline__ static void sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * C::warps) : "memory");
   }
-  float acc[C::NT][4];
+
+  // done(pos, nt, sums): called by the first slice's warps with the sums of token tile nt over
+  // the item's K: words 2 i + c are row lane / 4 + 8 i of the warp's 16 and token
+  // 8 nt + 2 (lane % 4) + c; end(pos): by all multiplying threads after them.
+  template <class Done, class End>
+  __device__ __forceinline__ void consume(int item0, float *red, int warp, int lane, Done done,
+                                          End end) const {
+    const int r = warp / C::S, s = warp % C::S;
+    float acc[C::NT][4];
 #pragma unroll
-  for (int nt = 0; nt < C::NT; ++nt)
+    for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-  int st = 0, ld = C::P - 1;
-  while (cq.on) {
-    cp_wait<C::P - 2>();
-    __syncthreads();  // the stage has landed; every warp is done with the stage before it
-    if (pq.on) {
-      k.load_w(pq, ld);
-      k.load_x(pq, ld);
-      k.next(pq);
-    }
-    cp_commit();
-    if (++ld == C::P) ld = 0;
-    k.multiply(cq, st, acc);
-    if (++st == C::P) st = 0;
-    if (cq.chunk == cq.c1 - 1) {
-      const int ntl = (min(cq.cnt, 8 * C::NT) + 7) >> 3;
-      // slices past the first hand over their sums (red is next written after the stage
-      // barrier of a later iteration)
-      float4 *part = reinterpret_cast<float4 *>(red) + k.r * C::NT * 32 + k.lane;
+      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+    int st = 0;
+    uint32_t phase = 0;
+    for (FewPos q = first(item0); q.on; next(q)) {
+      if (!mbar_wait(&full[st], phase, p.status, abort_flag)) *abort_flag = 1;
+      multiply(q, st, r, s, lane, acc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (++st == C::P) {
+        st = 0;
+        phase ^= 1u;
+      }
+      if (q.chunk < q.c1 - 1) continue;
+      const int ntl = (min(q.cnt, 8 * C::NT) + 7) >> 3;
+      // slices past the first hand over their sums
+      float4 *part4 = reinterpret_cast<float4 *>(red) + r * C::NT * 32 + lane;
       if (C::S > 1) {
-        if (k.s > 0) {
+        if (s > 0) {
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt)
             if (nt < ntl)
-              part[((k.s - 1) * C::R * C::NT + nt) * 32] =
+              part4[((s - 1) * C::R * C::NT + nt) * 32] =
                   make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
         }
-        __syncthreads();
+        sync();
       }
-      if (k.s == 0) {
+      if (s == 0) {
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
           if (nt < ntl) {
 #pragma unroll
-            for (int q = 0; q < C::S - 1; ++q) {
-              const float4 v = part[(q * C::R * C::NT + nt) * 32];
+            for (int o = 0; o < C::S - 1; ++o) {
+              const float4 v = part4[(o * C::R * C::NT + nt) * 32];
               acc[nt][0] += v.x;
               acc[nt][1] += v.y;
               acc[nt][2] += v.z;
               acc[nt][3] += v.w;
             }
-            done(cq, nt, acc[nt]);
+            done(q, nt, r, acc[nt]);
           }
         }
       }
-      end(cq);
+      end(q);
+      if (C::S > 1) sync();  // the partial sums are read before they are written again
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
     }
-    k.next(cq);
   }
-  cp_wait<0>();
+};
+
+// The CTA's dynamic shared memory from the first 1024-byte boundary on; barriers set up (the
+// caller synchronises the CTA before they are used).
+template <class C>
+__device__ __forceinline__ uint8_t *few_setup(uint8_t *raw, uint64_t *&full, uint64_t *&empty,
+                                              volatile int *&abort_flag) {
+  uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  full = reinterpret_cast<uint64_t *>(smem + C::o_bars);
+  empty = full + C::P;
+  abort_flag = reinterpret_cast<volatile int *>(smem + C::o_bars + 120);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::P; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], C::warps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  return smem;
 }
 
 template <class C>
 __global__ void __launch_bounds__(C::threads, C::min_ctas)
     k_few_glu(const __grid_constant__ FewParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
+  extern __shared__ uint8_t raw[];
   __shared__ int s_act;
+  uint64_t *full, *empty;
+  volatile int *abort_flag;
+  uint8_t *smem = few_setup<C>(raw, full, empty, abort_flag);
+  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
   pdl_wait();
   pdl_trigger();
   const int na = few_lists<C::threads>(p, l, &s_act);
-  FewKernel<C> k(p, l, smem_u32(smem));
-  k.item_end = na * k.tiles;
-  k.item_step = gridDim.x;
+  const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.h,
+                       (p.h + C::CH - 1) / C::CH, na, p.f / C::outs, (int)gridDim.x, 0, 0};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == C::warps) {
+    k.produce(blockIdx.x, false, lane);
+    return;
+  }
   float *hb = reinterpret_cast<float *>(smem + C::o_hbuf);
-  const int g = k.lane >> 2, t2 = 2 * (k.lane & 3);
-  few_stream(
-      k, blockIdx.x, reinterpret_cast<float *>(smem + C::o_red), false,
-      [&](const FewPos &q, int nt, const float (&v)[4]) {
+  const int g = lane >> 2, t2 = 2 * (lane & 3);
+  k.consume(
+      blockIdx.x, reinterpret_cast<float *>(smem + C::o_red), warp, lane,
+      [&](const FewPos &q, int nt, int r, const float (&v)[4]) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // gate v[c], up v[2 + c] of column f, token n
-          const int n = 8 * nt + t2 + c, col = k.r * 8 + g;
+        for (int c = 0; c < 2; ++c) {  // gate v[c], up v[2 + c] of one column and token n
+          const int n = 8 * nt + t2 + c, col = r * 8 + g;
           if (n >= q.cnt) continue;
           const uint32_t en = l.ent[q.n0 + n];
           if constexpr (C::MX4) {
@@ -694,7 +722,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
             hb[n * C::hrow + col] = silu_f(v[c] * xs) * (v[2 + c] * xs);
           } else {
             const float hv = silu_f(v[c]) * v[2 + c];
-            const size_t at = (size_t)(en & 0xFFFFu) * p.f + q.tile * C::outs + col;
+            const size_t at = (size_t)(en & 0xFFFFu) * p.f + q.b * C::outs + col;
             const __nv_bfloat16 hi = __float2bfloat16(hv);
             const float rest = hv - __bfloat162float(hi);
             p.hout[at] = __bfloat16_as_ushort(hi);
@@ -705,59 +733,72 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
       },
       [&](const FewPos &q) {
         if constexpr (C::MX4) {  // blocks of 32 columns to fp16, a warp each
-          __syncthreads();
+          k.sync();
           const int nr = min(q.cnt, 8 * C::NT);
-          for (int i = k.warp; i < nr * (C::outs / 32); i += C::warps) {
+          for (int i = warp; i < nr * (C::outs / 32); i += C::warps) {
             const int n = i / (C::outs / 32), b = i % (C::outs / 32);
-            const float hv = hb[n * C::hrow + b * 32 + k.lane];
+            const float hv = hb[n * C::hrow + b * 32 + lane];
             const int es =
                 f16_block_exp(__reduce_max_sync(0xFFFFFFFFu, finite_abs(__float_as_uint(hv))));
             const size_t at =
-                (size_t)(l.ent[q.n0 + n] & 0xFFFFu) * p.f + q.tile * C::outs + b * 32 + k.lane;
+                (size_t)(l.ent[q.n0 + n] & 0xFFFFu) * p.f + q.b * C::outs + b * 32 + lane;
             p.hout[at] = __half_as_ushort(__float2half_rn(hv * pow2(es)));
-            if (k.lane == 0) p.hscale[at >> 5] = pow2(-es);
+            if (lane == 0) p.hscale[at >> 5] = pow2(-es);
           }
+          if (C::S == 1) k.sync();  // hb is read before the next tile writes it
         }
       });
 }
 
 // A cluster of G CTAs shares a row tile, each with every G-th of the experts in use (neighbouring
-// experts of a skewed router hold similar numbers of tokens); their sums are added in rank
-// order through distributed shared memory.
+// experts of a skewed router hold similar numbers of tokens) or parts of K; their sums are
+// added in rank order through distributed shared memory.
 template <class C>
 __global__ void __launch_bounds__(C::threads, C::min_ctas)
     k_few_down(const __grid_constant__ FewParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t raw[];
+  __shared__ int s_act;
+  uint64_t *full, *empty;
+  volatile int *abort_flag;
+  uint8_t *smem = few_setup<C>(raw, full, empty, abort_flag);
   const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
   float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p.E, p.T * p.k));
-  __shared__ int s_act;
   // Before the wait for k_few_glu: only what was complete when that kernel passed its own
   // wait (it lets this one start after that): the routing, and the caller's W2.
   const int na = few_lists<C::threads>(p, l, &s_act);
   const int G = p.groups, rank = (int)cluster_ctarank();
-  FewKernel<C> k(p, l, smem_u32(smem));
-  k.fixed_tile = blockIdx.x / G;
-  k.item_end = na * p.kparts;
-  k.item_step = G;
+  const int chunks = (p.f + C::CH - 1) / C::CH;
+  const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.f, chunks, na,
+                       p.kparts, G, (int)blockIdx.x / G, (chunks + p.kparts - 1) / p.kparts};
   for (int i = threadIdx.x; i < p.T * C::yrow; i += C::threads) ysum[i] = 0.0f;
-  const int g = k.lane >> 2, t2 = 2 * (k.lane & 3);
-  few_stream(
-      k, rank, reinterpret_cast<float *>(smem + C::o_red), true,
-      [&](const FewPos &q, int nt, const float (&v)[4]) {
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == C::warps) {
+    k.produce(rank, true, lane);
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    const int g = lane >> 2, t2 = 2 * (lane & 3);
+    k.consume(
+        rank, reinterpret_cast<float *>(smem + C::o_red), warp, lane,
+        [&](const FewPos &q, int nt, int r, const float (&v)[4]) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = 8 * nt + t2 + c;
-          if (n >= q.cnt) continue;
-          const uint32_t en = l.ent[q.n0 + n];  // an expert's entries belong to distinct tokens
-          const float w = few_weight(p, en & 0xFFFFu, q.e);
-          float *y = ysum + (en >> 16) * C::yrow + k.r * 16 + g;
-          y[0] = fmaf(w, v[c], y[0]);
-          y[8] = fmaf(w, v[2 + c], y[8]);
-        }
-      },
-      [](const FewPos &) {});
+          for (int c = 0; c < 2; ++c) {
+            const int n = 8 * nt + t2 + c;
+            if (n >= q.cnt) continue;
+            const uint32_t en = l.ent[q.n0 + n];  // an expert's entries: distinct tokens
+            const float w = few_weight(p, en & 0xFFFFu, q.e);
+            float *y = ysum + (en >> 16) * C::yrow + r * 16 + g;
+            y[0] = fmaf(w, v[c], y[0]);
+            y[8] = fmaf(w, v[2 + c], y[8]);
+          }
+          __syncwarp();  // another lane may add to these sums for the next expert
+        },
+        [](const FewPos &) {});
+  }
+  __syncwarp();
   cluster_sync_all();
-  const int h0 = k.fixed_tile * C::outs;
+  const int h0 = k.tile * C::outs;
   const uint32_t mine = smem_u32(ysum);
   for (int i = rank * C::threads + threadIdx.x; i < p.T * (C::outs / 2); i += G * C::threads) {
     const int t = i / (C::outs / 2), c = 2 * (i % (C::outs / 2));
@@ -791,12 +832,33 @@ cudaError_t allow_smem(Kernel kernel, std::atomic<uint64_t> &done) {
   return e;
 }
 
+// Weights [rows, K] as slices of SC columns: {SC, rows, K / SC}; a box is a tile's rows of all the
+// slices of a stage (slices past K read zeros).
 template <class C>
-cudaError_t launch_few_glu(const FewParams &p, cudaStream_t st) {
+bool few_map(CUtensorMap *m, const void *ptr, long long rows, int K) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t pitch = (cuuint64_t)K * (C::MX4 ? 1 : 4) / 2;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(K / C::SC)};
+  cuuint64_t strides[2] = {pitch, (cuuint64_t)C::row_b};
+  cuuint32_t box[3] = {64, (cuuint32_t)C::rows_m, (cuuint32_t)C::slices}, estr[3] = {1, 1, 1};
+  return enc(m, C::MX4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             C::MX4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(k_few_glu<C>, done);
   if (e != cudaSuccess) return e;
-  const size_t smem = C::o_lists + few_list_bytes(p.E, p.T * p.k);
+  const long long ef = (long long)p.E * p.f;
+  if (!few_map<C>(&p.tw[0], p.w1.data, ef, p.h) || !few_map<C>(&p.tw[1], p.w3.data, ef, p.h))
+    return cudaErrorInvalidValue;
+  p.ws[0] = static_cast<const uint8_t *>(p.w1.scales);
+  p.ws[1] = static_cast<const uint8_t *>(p.w3.scales);
+  const size_t smem = C::fixed + few_list_bytes(p.E, p.T * p.k);
   const long long n = (long long)p.T * p.k;
   const long long items = (n < p.E ? n : p.E) * (p.f / C::outs);
   long long ctas = device_sm_count();
@@ -809,8 +871,11 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(k_few_down<C>, done);
   if (e != cudaSuccess) return e;
-  const size_t smem = C::o_lists + few_list_bytes(p.E, p.T * p.k) +
-                      (size_t)p.T * C::yrow * sizeof(float);
+  if (!few_map<C>(&p.tw[0], p.w2.data, (long long)p.E * p.h, p.f)) return cudaErrorInvalidValue;
+  p.tw[1] = p.tw[0];
+  p.ws[0] = p.ws[1] = static_cast<const uint8_t *>(p.w2.scales);
+  const size_t smem = C::fixed + few_list_bytes(p.E, p.T * p.k) +
+                      (size_t)p.T * C::y_row_bytes;
   const long long n = (long long)p.T * p.k;
   const int experts = (int)(n < p.E ? n : p.E);
   const int tiles = p.h / C::outs;
@@ -855,6 +920,7 @@ cudaError_t launch_few_pair(const FewParams &p, const FewParams &d, cudaStream_t
 cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renorm, int32_t *top,
                        float *weights, int32_t *status, cudaStream_t st) {
   FewParams p = p_in;
+  p.status = status;
   const bool mx4 = p.w1.scales != nullptr;
   cudaError_t e = launch_pdl(k_few_route, p.T, mx4 ? 32 * kRouteWarps : 32, 0, st, logits, p.E, p.k,
                              renorm ? 1 : 0, p.h, top, weights, status,

@@ -1,6 +1,7 @@
 // kernels.h -- host-side launchers of the dMoE kernels (internal to libdmoe.so).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -180,6 +181,9 @@ struct FewParams {
   const uint16_t *xin, *xlo;
   const float *xscale;
   int groups, kparts;
+  CUtensorMap tw[2];  // W1 and W3, or W2
+  const uint8_t *ws[2];
+  int32_t *status;
 };
 // logits given: top and weights are written first; else they are inputs.
 cudaError_t launch_few(const FewParams &p, const uint16_t *logits, bool renorm, int32_t *top,
