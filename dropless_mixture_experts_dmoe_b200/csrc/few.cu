@@ -183,63 +183,56 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
                    smem_u32(bar))
                : "memory");
 }
+// Shared-memory reads of the products: volatile, so that they stay behind the barrier waits, but
+// without claiming other memory, so that the compiler moves them among the products.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same with a zero accumulator going in.
-__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+// d = a b + c
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
 }
 
 // Shape of a variant: MX4 weights in four bits; DOWN the second product; NT tiles of 8 tokens;
 // R x S multiplying warps of KU columns; P stages.  BR: copies of the token rows (two: H's
 // upper and lower bf16).  SB: the token operand has a scale per 32 columns (H in fp16).
-template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int KU_, int P_>
+template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int KU_, int P_, int CTAS_,
+          bool WIDE_ = false>
 struct FewCfg {
-  static constexpr bool MX4 = MX4_, DOWN = DOWN_, SB = MX4 && DOWN;
+  static constexpr bool MX4 = MX4_, DOWN = DOWN_, SB = MX4 && DOWN, WIDE = WIDE_;
   static constexpr int NT = NT_, R = R_, S = S_, KU = KU_, P = P_;
   static constexpr int warps = R * S, threads = 32 * warps + 32;
-  static constexpr int min_ctas = warps == 8 ? 2 : 1;
+  static constexpr int min_ctas = CTAS_;  // CTAs per SM
   static constexpr int CH = S * KU;  // columns per stage
   static constexpr int BR = (DOWN && !MX4) ? 2 : 1;
   // weights: [W1, W3 | W2][slices of SC columns][rows][row_b bytes], as TMA boxes land
-  static constexpr int SC = MX4 ? 128 : 64, slices = CH / SC;
-  static constexpr int row_b = MX4 ? 64 : 128;
+  static constexpr int SC = MX4 ? (WIDE ? 256 : 128) : 64, slices = CH / SC;
+  static constexpr int row_b = MX4 && !WIDE ? 64 : 128;
   static constexpr int mats = DOWN ? 1 : 2, rows_m = DOWN ? 16 * R : 8 * R;
   static constexpr int w_mat = slices * rows_m * row_b, w_bytes = mats * w_mat;
   static constexpr int sc_mat = MX4 ? CH / 128 * kMx4TileBytes : 0;  // whole scale tiles
@@ -483,23 +476,22 @@ struct FewKernel {
 
   // ---- the multiplying warps ----
 
-  // Whether a byte of w is 0 or 255 (exact for "any": a borrow needs a zero byte below it).
-  __device__ __forceinline__ static bool odd_scales(uint32_t w) {
-    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
-  }
-
-  // Four blocks (128 columns, a slice) of a warp's 16 rows times the token tiles.  wl: this
-  // lane's word of row lane / 4 in the slice; xb, sb: its token row and the token scales.
-  template <bool ODD>
+  // Four blocks (128 columns, a slice) of a warp's 16 rows times the token tiles, added to acc
+  // times two (done() halves the sums): 2^(s - 126) has the exponent field s + 1, which is
+  // right for every s up to 253, 0 included.  LARGE: for scale bytes above 127 in the stage (254
+  // and 255, NaN, among them), the factor 2^(s - 127) made case by case.  wl: this lane's word of
+  // row lane / 4 in the slice; xb, sb: its token row and the token scales.
+  template <bool LARGE>
   __device__ __forceinline__ void blocks(uint32_t wl, uint32_t xb, uint32_t sb, uint32_t sca,
-                                         uint32_t scb, int ntl, float (&acc)[C::NT][4]) const {
+                                         uint32_t scb, int ntl, const float (&zero)[4],
+                                         float (&acc)[C::NT][4]) const {
     constexpr int up = C::DOWN ? 8 * C::row_b : C::w_mat;  // from row i to row i + 8
     constexpr bool ahead = C::SB && C::NT <= 2;  // a slice's token scales fit in registers
     uint32_t s0[C::NT][4], s1[C::NT][4];
     if constexpr (ahead) {
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
-        if (nt >= ntl) break;
+        if (nt > 0 && nt >= ntl) break;
         lds128(s0[nt], sb + nt * 8 * C::sb_row);
         lds128(s1[nt], sb + (nt * 8 + 1) * C::sb_row);
       }
@@ -511,21 +503,21 @@ struct FewKernel {
       mx4_unpack8(lds32(wa), lo);
       mx4_unpack8(lds32(wa + up), hi);
       float fa, fb;
-      if (ODD) {
+      if (LARGE) {
         fa = mx4_scale_value((sca >> (8 * b)) & 0xFFu);
         fb = mx4_scale_value((scb >> (8 * b)) & 0xFFu);
-      } else {
+      } else {  // sca, scb: the bytes plus one
         fa = __uint_as_float((b < 3 ? sca << (23 - 8 * b) : sca >> 1) & 0x7F800000u);
         fb = __uint_as_float((b < 3 ? scb << (23 - 8 * b) : scb >> 1) & 0x7F800000u);
       }
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
-        if (nt >= ntl) break;
+        if (nt > 0 && nt >= ntl) break;
         uint32_t x[4];
         lds128(x, xb + nt * 8 * C::x_row + b * 64);
-        float c[4];
-        mma_f16_zero(c, lo[0], hi[0], lo[1], hi[1], x[0], x[1]);
-        mma_f16(c, lo[2], hi[2], lo[3], hi[3], x[2], x[3]);
+        float h[4], c[4];
+        mma_f16(h, lo[0], hi[0], lo[1], hi[1], x[0], x[1], zero);
+        mma_f16(c, lo[2], hi[2], lo[3], hi[3], x[2], x[3], h);
         if constexpr (C::SB) {
           if constexpr (!ahead) {
             s0[nt][b] = lds32(sb + nt * 8 * C::sb_row + 4 * b);
@@ -537,6 +529,10 @@ struct FewKernel {
           c[2] *= u;
           c[3] *= v;
         }
+        if (LARGE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] += c[i];
+        }
         acc[nt][0] = fmaf(c[0], fa, acc[nt][0]);
         acc[nt][1] = fmaf(c[1], fa, acc[nt][1]);
         acc[nt][2] = fmaf(c[2], fb, acc[nt][2]);
@@ -545,7 +541,9 @@ struct FewKernel {
     }
   }
 
-  __device__ __forceinline__ void multiply(const FewPos &q, int st, int r, int s, int lane,
+  // tile0: the item's first row within its 128-row scale tile.
+  __device__ __forceinline__ void multiply(const FewPos &q, int tile0, int st, int r, int s,
+                                           int lane, const float (&zero)[4],
                                            float (&acc)[C::NT][4]) const {
     const int left = K - q.chunk * C::CH - s * C::KU;
     if (left <= 0) return;
@@ -554,25 +552,39 @@ struct FewKernel {
     if constexpr (C::MX4) {
       const int g = lane >> 2, t = lane & 3;
       const int row = r * (C::DOWN ? 16 : 8) + g;  // of the box
-      const uint32_t w = base + s * (C::KU / 128) * C::rows_m * 64 + row * 64 +
-                         (((row >> 1) & 3) << 4) + 4 * t;
+      constexpr int js = C::KU / 128;
+      // this lane's word of block 0 (an exclusive or with 16 b gives block b's: the boxes are
+      // swizzled by row, 64-byte rows every second one)
+      const uint32_t w = base + s * (C::KU / C::SC) * C::rows_m * C::row_b + row * C::row_b +
+                         ((C::WIDE ? row & 7 : (row >> 1) & 3) << 4) + 4 * t;
+      auto wj = [&](int j) {  // 128 columns on
+        return C::WIDE ? (w + (j >> 1) * C::rows_m * 128) ^ ((j & 1) << 6) : w + j * C::rows_m * 64;
+      };
       // the tile's rows start at a multiple of 8: rows 0..7 and 8..15 stay in one 32-row group
-      const int r128 = (tile_of(q) * C::outs + row) & 127;
-      const uint32_t sw = base + C::o_sc + s * (C::KU / 128) * kMx4TileBytes + (r128 & 31) * 16 +
-                          (r128 >> 5) * 4;
+      const int r128 = tile0 + row;
+      const uint32_t sw =
+          base + C::o_sc + s * js * kMx4TileBytes + (r128 & 31) * 16 + (r128 >> 5) * 4;
       constexpr int sup = C::DOWN ? 128 : C::sc_mat;
       const uint32_t xb = base + C::o_x + g * C::x_row + (s * C::KU + 8 * t) * 2;
       const uint32_t sb = base + C::o_sb + 2 * t * C::sb_row + s * (C::KU / 8);
+      uint32_t sca[js], scb[js], any = 0u;
 #pragma unroll
-      for (int j = 0; j < C::KU / 128; ++j) {
-        if (j * 128 >= left) break;
-        const uint32_t sca = lds32(sw + j * kMx4TileBytes);
-        const uint32_t scb = lds32(sw + j * kMx4TileBytes + sup);
-        // scale bytes 1 .. 254 are exponent fields as they stand; 0 (2^-127) and 255 (NaN) are not
-        if (__any_sync(0xFFFFFFFFu, odd_scales(sca) | odd_scales(scb)))
-          blocks<true>(w + j * C::rows_m * 64, xb + j * 256, sb + j * 16, sca, scb, ntl, acc);
-        else
-          blocks<false>(w + j * C::rows_m * 64, xb + j * 256, sb + j * 16, sca, scb, ntl, acc);
+      for (int j = 0; j < js; ++j) {  // (the slice past an odd end holds an earlier stage's)
+        sca[j] = lds32(sw + j * kMx4TileBytes);
+        scb[j] = lds32(sw + j * kMx4TileBytes + sup);
+        any |= sca[j] | scb[j];
+      }
+      if (__any_sync(0xFFFFFFFFu, any & 0x80808080u)) {
+#pragma unroll
+        for (int j = 0; j < js; ++j)
+          if (j * 128 < left)
+            blocks<true>(wj(j), xb + j * 256, sb + j * 16, sca[j], scb[j], ntl, zero, acc);
+      } else {
+#pragma unroll
+        for (int j = 0; j < js; ++j)
+          if (j * 128 < left)
+            blocks<false>(wj(j), xb + j * 256, sb + j * 16, sca[j] + 0x01010101u,
+                          scb[j] + 0x01010101u, ntl, zero, acc);
       }
     } else {
       const int ar = lane & 15;
@@ -587,7 +599,7 @@ struct FewKernel {
         ldsm4(a1, wr + (((2 * kk + 2 + (lane >> 4)) ^ (ar & 7)) << 4));
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
-          if (nt >= ntl) break;
+          if (nt > 0 && nt >= ntl) break;
 #pragma unroll
           for (int br = 0; br < C::BR; ++br) {
             uint32_t x[4];
@@ -617,11 +629,17 @@ struct FewKernel {
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+    // four zero registers, kept: the accumulator that each block's first product starts from
+    float zero[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     int st = 0;
     uint32_t phase = 0;
+    int tile0 = 0;
     for (FewPos q = first(item0); q.on; next(q)) {
+      if (C::MX4 && q.chunk == q.c0) tile0 = (tile_of(q) * C::outs) & 127;
       if (!mbar_wait(&full[st], phase, p.status, abort_flag)) *abort_flag = 1;
-      multiply(q, st, r, s, lane, acc);
+      multiply(q, tile0, st, r, s, lane, zero, acc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       if (++st == C::P) {
@@ -718,7 +736,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
           if (n >= q.cnt) continue;
           const uint32_t en = l.ent[q.n0 + n];
           if constexpr (C::MX4) {
-            const float xs = __ldg(p.xscale + (en >> 16));
+            const float xs = 0.5f * __ldg(p.xscale + (en >> 16));
             hb[n * C::hrow + col] = silu_f(v[c] * xs) * (v[2 + c] * xs);
           } else {
             const float hv = silu_f(v[c]) * v[2 + c];
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
             const int n = 8 * nt + t2 + c;
             if (n >= q.cnt) continue;
             const uint32_t en = l.ent[q.n0 + n];  // an expert's entries: distinct tokens
-            const float w = few_weight(p, en & 0xFFFFu, q.e);
+            const float w = few_weight(p, en & 0xFFFFu, q.e) * (C::MX4 ? 0.5f : 1.0f);
             float *y = ysum + (en >> 16) * C::yrow + r * 16 + g;
             y[0] = fmaf(w, v[c], y[0]);
             y[8] = fmaf(w, v[2 + c], y[8]);
@@ -839,13 +857,21 @@ bool few_map(CUtensorMap *m, const void *ptr, long long rows, int K) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t pitch = (cuuint64_t)K * (C::MX4 ? 1 : 4) / 2;
-  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(K / C::SC)};
+  const cuuint32_t dim0 = C::MX4 ? C::row_b : 64;  // bytes, or bf16
+  cuuint64_t dims[3] = {dim0, (cuuint64_t)rows, (cuuint64_t)(K / C::SC)};
   cuuint64_t strides[2] = {pitch, (cuuint64_t)C::row_b};
-  cuuint32_t box[3] = {64, (cuuint32_t)C::rows_m, (cuuint32_t)C::slices}, estr[3] = {1, 1, 1};
+  cuuint32_t box[3] = {dim0, (cuuint32_t)C::rows_m, (cuuint32_t)C::slices}, estr[3] = {1, 1, 1};
   return enc(m, C::MX4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
              const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             C::MX4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             C::row_b == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of `smem` bytes that the device holds at once (1 KB of each is the system's).
+template <class C>
+int few_places(size_t smem) {
+  const int n = (int)(228 * 1024 / (smem + 1024 + 64));
+  return device_sm_count() * (n < 1 ? 1 : n < C::min_ctas ? n : C::min_ctas);
 }
 
 template <class C>
@@ -861,8 +887,7 @@ cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   const size_t smem = C::fixed + few_list_bytes(p.E, p.T * p.k);
   const long long n = (long long)p.T * p.k;
   const long long items = (n < p.E ? n : p.E) * (p.f / C::outs);
-  long long ctas = device_sm_count();
-  if (2 * (smem + 2048) <= 228 * 1024 && C::min_ctas > 1) ctas *= 2;
+  const long long ctas = few_places<C>(smem);
   return launch_pdl(k_few_glu<C>, (int)(items < ctas ? items : ctas), C::threads, smem, st, p);
 }
 
@@ -881,8 +906,7 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   const int tiles = p.h / C::outs;
   // the experts are spread over up to eight CTAs per row tile until there is one CTA for each
   // place on the SMs; with fewer experts than that, K is cut into parts as well (whole chunks)
-  int places = device_sm_count();
-  if (2 * (smem + 2048) <= 228 * 1024 && C::min_ctas > 1) places *= 2;
+  const int places = few_places<C>(smem);
   int G = 1;
   while (G < 8 && tiles * G * 2 <= places) G *= 2;
   const int chunks = (p.f + C::CH - 1) / C::CH;
@@ -908,11 +932,17 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_few_down<C>, p);
 }
 
-template <bool MX4, int NT, int R, int S, int KU, int PG, int PD>
+// 4-bit weights whose rows are whole 128-byte pieces (K a multiple of 256) are fetched in boxes of
+// 128-byte rows, others in boxes of 64-byte rows.
+template <bool MX4, int NT, int R, int S, int KU, int PG, int CG, int PD, int CD>
 cudaError_t launch_few_pair(const FewParams &p, const FewParams &d, cudaStream_t st) {
-  cudaError_t e = launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG>>(p, st);
+  cudaError_t e = MX4 && p.h % 256 == 0
+                      ? launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG, CG, MX4>>(p, st)
+                      : launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG, CG>>(p, st);
   if (e != cudaSuccess) return e;
-  return launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD>>(d, st);
+  return MX4 && p.f % 256 == 0
+             ? launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD, CD, MX4>>(d, st)
+             : launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD, CD>>(d, st);
 }
 
 }  // namespace
@@ -938,16 +968,17 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   const double mean = (double)p.T * p.k / p.E;
   int nt = p.T <= 8 || mean <= 3 ? 1 : p.T <= 16 || mean <= 8 ? 2 : p.T <= 32 || mean <= 20 ? 4 : 8;
   if (var) nt = var;
+  const long long n = (long long)p.T * p.k, used = n < p.E ? n : p.E;
   if (mx4) {
-    if (nt == 1) return launch_few_pair<true, 1, 4, 2, 256, 3, 3>(p, d, st);
-    if (nt == 2) return launch_few_pair<true, 2, 4, 2, 128, 4, 4>(p, d, st);
-    if (p.T <= 32) return launch_few_pair<true, 4, 8, 2, 128, 4, 4>(p, d, st);
-    return launch_few_pair<true, 4, 8, 2, 128, 4, 3>(p, d, st);
+    if (var ? var == 16 : used * (p.f / 64) < device_sm_count() && nt == 1) return launch_few_pair<true, 1, 4, 2, 256, 3, 2, 3, 2>(p, d, st);
+    if (nt == 1) return launch_few_pair<true, 1, 8, 1, 256, 3, 3, 3, 3>(p, d, st);
+    if (nt == 2) return launch_few_pair<true, 2, 8, 1, 256, 3, 2, 3, 2>(p, d, st);
+    return launch_few_pair<true, 4, 8, 1, 256, 2, 2, 2, 2>(p, d, st);
   }
-  if (nt == 1) return launch_few_pair<false, 1, 1, 8, 64, 4, 3>(p, d, st);
-  if (nt == 2) return launch_few_pair<false, 2, 2, 4, 64, 4, 3>(p, d, st);
-  if (nt == 4) return launch_few_pair<false, 4, 4, 2, 64, 3, 3>(p, d, st);
-  return launch_few_pair<false, 8, 8, 1, 64, 3, 3>(p, d, st);
+  if (nt == 1) return launch_few_pair<false, 1, 1, 8, 64, 4, 2, 3, 2>(p, d, st);
+  if (nt == 2) return launch_few_pair<false, 2, 2, 4, 64, 4, 2, 3, 2>(p, d, st);
+  if (nt == 4) return launch_few_pair<false, 4, 4, 2, 64, 3, 2, 3, 2>(p, d, st);
+  return launch_few_pair<false, 8, 8, 1, 64, 3, 2, 3, 2>(p, d, st);
 }
 
 }  // namespace dmoe
