@@ -6,21 +6,25 @@
 //         (a thread holds a row's 32-column block, so its maximum needs no exchange)
 //   DOWN  Y_pad = w * (H W2_e^T) in block floating point, as the bf16 down GEMM writes it
 //
-// One SM pair per tile (cta_group::2, M = 256, N = 256): at four bits a 128 x 256 tile on one
-// SM would need 100 bytes of operands per clock from L2; the pair needs 66.  The unit of work is
-// a pair of consecutive row blocks of one expert times a column tile, enumerated from
-// padded_bins on the device.  Persistent clusters of two CTAs, 320 threads each:
+// One SM pair per tile (cta_group::2, M = 256): at four bits a 128 x 256 tile on one SM would need
+// 100 bytes of operands per clock from L2; a pair's 256 x 256 needs 66.  The unit of work is a
+// pair of consecutive row blocks of one expert times a column tile, enumerated from padded_bins
+// on the device.  GLU tiles are 256 columns wide (128 of gate, 128 of up).  DOWN tiles are 128
+// wide with two accumulators: its K (ffn) is short, so that the hand-over of the accumulator,
+// not the operands, bounds it.  Persistent clusters of two CTAs, 576 threads each:
 //   warp 0      TMA producer: per stage of 256 K this CTA's 128 rows of A (16 KB, 128-byte
-//               swizzle), its half of B (16 KB), the scale tiles of its A rows (1 KB) and of
-//               all 256 rows of B (2 KB; each SM of the pair multiplies by all of them)
-//   warp 1      one thread of the leader: tcgen05.cp of the stage's scale tiles into tensor memory
-//               (six 512-byte tiles, each 32 lanes x 4 columns repeated for the four lane
-//               groups), then four MMAs of 64 K
-//   warps 2..9  epilogue: a warp takes 32 rows and half of the columns
+//               swizzle), its half of B, the scale tiles of its A rows and of all rows of B (each
+//               SM of the pair multiplies by all of them)
+//   warp 1      one thread of the leader: tcgen05.cp of a stage's scale tiles into tensor memory
+//               (512-byte tiles, each 32 lanes x 4 columns repeated for the four lane groups) and
+//               four MMAs of 64 K.  The copies of the next stage go ahead of the MMAs of the
+//               current one when its data is there: the tensor pipe takes both in order, and an
+//               MMA right behind its own scales waits for them
+//   warps 2..17 epilogue: a warp takes 32 rows and 64 accumulator columns
 // Tensor memory: 256 accumulator columns, and 32 columns of scales per stage, which are
-// rewritten only after the stage's MMAs are done.  Two accumulators and scales do not
-// fit in 512 columns; instead the epilogue takes its 128 columns into registers at once and
-// releases the accumulator before it converts and stores them.
+// rewritten only after the stage's MMAs are done.  Two GLU accumulators and scales do not fit in
+// 512 columns; instead an epilogue warp takes its 64 columns into registers at once and releases
+// the accumulator before it converts and stores them.
 //
 // Every mbarrier wait is bounded; on expiry the kernel sets DMOE_STATUS_TIMEOUT, raises an
 // abort flag for the other roles of its CTA, drains what it issued and returns.
@@ -36,23 +40,34 @@ namespace dmoe {
 
 namespace {
 
-constexpr int XM = 128;           // rows per CTA
-constexpr int XN = 256;           // columns per tile
-constexpr int XK = 256;           // K per stage: one 128-byte swizzle row of elements
-constexpr int X_OP = XM * XK / 2;  // an operand's bytes per stage and CTA: 16 KB
-constexpr int X_SFA = 2 * kMx4TileBytes;  // two column tiles of scales
-constexpr int X_SFB = 4 * kMx4TileBytes;  // ... of both 128-row tiles of B
-constexpr int X_STAGE = 2 * X_OP + X_SFA + X_SFB;  // 35 KB
-constexpr int X_STAGES = 5;
-constexpr int X_EPI = 8;
+constexpr int XM = 128;            // rows per CTA
+constexpr int XK = 256;            // K per stage: one 128-byte swizzle row of elements
+constexpr int X_A = XM * XK / 2;   // A's bytes per stage and CTA: 16 KB
+constexpr int X_SF = 2 * kMx4TileBytes;  // scales of 128 rows: two column tiles
+constexpr int X_EPI = 16;
 constexpr int X_THREADS = 64 + 32 * X_EPI;
 constexpr int X_BOX = 32 * 128;  // a result box: 32 rows x 128 B
 constexpr int X_TMEM = 512;
-constexpr int X_SF_COL = 256;     // scales of stage s: columns 256 + 32 s ..
-static_assert(X_SF_COL + 32 * X_STAGES <= X_TMEM, "tensor memory");
-constexpr size_t X_SMEM = 1024 + (size_t)X_STAGES * X_STAGE + X_EPI * X_BOX + 256 +
-                          sizeof(int) * (DMOE_MAX_EXPERTS + 1);
-static_assert(X_SMEM <= 227 * 1024, "shared memory");
+constexpr int X_SF_COL = 256;  // scales of stage s: columns 256 + 32 s ..
+
+// DOWN stages its results in one box per epilogue warp, GLU stores from registers.
+template <bool GLU>
+struct MxCfg {
+  static constexpr int N = GLU ? 256 : 128;  // columns per tile (accumulator)
+  static constexpr int nacc = GLU ? 1 : 2;
+  static constexpr int sfb = N / 128;            // 128-row scale tiles of B
+  static constexpr int b_bytes = N / 2 * XK / 2;  // this CTA's half of B
+  static constexpr int ops = X_A + b_bytes, sf = (1 + sfb) * X_SF, stage = ops + sf;
+  static constexpr int stages = GLU ? 6 : 5;
+  static constexpr int out = GLU ? 0 : X_EPI * X_BOX;
+  static constexpr int amax = GLU ? 0 : X_EPI * 32 * 4;
+  static constexpr size_t smem = 1024 + (size_t)stages * stage + out + amax + 256 +
+                                 sizeof(int) * (DMOE_MAX_EXPERTS + 1);
+  // arrivals that release an accumulator: the epilogue warps of both CTAs that read it
+  static constexpr int epi_arrivals = 2 * X_EPI / nacc;
+  static_assert(X_SF_COL + 32 * stages <= X_TMEM, "tensor memory");
+  static_assert(smem <= 227 * 1024, "shared memory");
+};
 
 struct MxParams {
   CUtensorMap ta, tsa;            // A elements and scales
@@ -135,38 +150,50 @@ __device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// One lane of a converged warp.  The producer and MMA warps run their loops as whole warps and
+// elect the lane only around the instructions: their operands then stay in uniform registers
+// (a loop of one lane moved every operand over, about 90 clocks an instruction).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ int mx_snake(int r, int cluster, int nclusters) {
   return r * nclusters + ((r & 1) ? nclusters - 1 - cluster : cluster);
 }
 
-// Two MX blocks (64 columns of H) of this thread's row from gate g and up u.
-__device__ __forceinline__ void glu_store(const MxParams &p, const uint32_t (&g)[2][32],
-                                          const uint32_t (&u)[2][32], int row, int n, int half) {
-  uint32_t sc[2];
-  uint4 *dst = reinterpret_cast<uint4 *>(p.hq + (size_t)row * (p.f >> 1) + n * 64 + half * 32);
+// silu(z) u with one reciprocal: e^-z overflowing to inf gives 1 / inf = 0, the limit.
+__device__ __forceinline__ float silu_mul(float z, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-z)));
+  return z * r * u;
+}
+
+// One block (32 columns of H) of this thread's row from gate g and up u, block `blk` of the row.
+__device__ __forceinline__ void glu_store(const MxParams &p, const uint32_t (&g)[32],
+                                          const uint32_t (&u)[32], int row, int blk) {
+  float v[32];
+  uint32_t m = 0u;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float v[32];
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = silu_f(__uint_as_float(g[j][i])) * __uint_as_float(u[j][i]);
-      m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    }
-    sc[j] = mx4_scale_byte(m);
-    const float inv = mx4_inverse(min(sc[j], 252u));
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = v[8 * q + i] * inv;
-      w[q] = (sc[j] == 255u) ? 0u : mx4_pack8(o);
-    }
-    dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 32; ++i) {
+    v[i] = silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i]));
+    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
-  *reinterpret_cast<uint16_t *>(p.hs + mx4_scale_word(row, n, p.f >> 7) + 2 * half) =
-      (uint16_t)(sc[0] | (sc[1] << 8));
+  const uint32_t sc = mx4_scale_byte(m);
+  const float inv = mx4_inverse(min(sc, 252u));
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[8 * q + i] * inv;
+    w[q] = (sc == 255u) ? 0u : mx4_pack8(o);
+  }
+  *reinterpret_cast<uint4 *>(p.hq + (size_t)row * (p.f >> 1) + blk * 16) =
+      make_uint4(w[0], w[1], w[2], w[3]);
+  p.hs[mx4_scale_word(row, blk >> 2, p.f >> 7) + (blk & 3)] = (uint8_t)sc;
 }
 
 template <bool GLU>
@@ -176,14 +203,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   const uint32_t base_u32 = smem_u32(smem_raw);
   uint8_t *tiles = smem_raw + ((1024u - (base_u32 & 1023u)) & 1023u);
   // operands of all stages first (1024-byte aligned), then result boxes, scales, barriers
-  uint8_t *outbuf = tiles + X_STAGES * 2 * X_OP;
-  uint8_t *scales = outbuf + X_EPI * X_BOX;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(scales + X_STAGES * (X_SFA + X_SFB));
+  using C = MxCfg<GLU>;
+  constexpr int X_STAGES = C::stages;
+  uint8_t *outbuf = tiles + X_STAGES * C::ops;
+  uint8_t *scales = outbuf + MxCfg<GLU>::out;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(scales + X_STAGES * C::sf);
   uint64_t *full = bars, *empty = bars + X_STAGES;
-  uint64_t *tfull = bars + 2 * X_STAGES, *tempty = tfull + 1, *drain = tfull + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 3);
+  uint64_t *tfull = bars + 2 * X_STAGES, *tempty = tfull + 2, *drain = tfull + 4;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  int *ustart = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 256);  // [E + 1]
+  float *amax = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bars) + 256);
+  int *ustart = reinterpret_cast<int *>(amax + MxCfg<GLU>::amax / 4);  // [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -195,8 +225,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * X_EPI);
+    for (int a = 0; a < C::nacc; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], C::epi_arrivals);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -236,9 +268,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   const int total = ustart[p.E] * p.n_tiles;
   const int k_stages = (p.k_tiles + 1) / 2;
   const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
-  const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
+  const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
     int stage = 0;
     uint32_t phase = 0;
@@ -247,29 +279,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     for (int r = 0, t = mx_snake(0, cluster, nclusters); ok && t < total;
          t = mx_snake(++r, cluster, nclusters)) {
       const MxTile tl = mx_decode(p, t, ustart, rank);
-      // B rows: this CTA's half; scale row tiles of both halves
-      const int brow = GLU ? tl.e * p.f + tl.n * (XN / 2)
-                           : tl.e * p.h + tl.n * XN + (int)rank * (XN / 2);
-      const int s0 = (GLU ? brow : tl.e * p.h + tl.n * XN) / 128;
-      const int s1 = GLU ? s0 : s0 + 1;
+      // B rows: this CTA's half; scale row tiles of all of B
+      const int brow =
+          GLU ? tl.e * p.f + tl.n * 128 : tl.e * p.h + tl.n * 128 + (int)rank * 64;
+      const int s0 = brow / 128 * p.k_tiles, sa0 = tl.row0 / 128 * p.k_tiles;
       for (int kb = 0; kb < k_stages; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag, p.wait_cycles)) {
           ok = false;
           break;
         }
         const uint32_t bar = leader_full0 + (uint32_t)(stage * sizeof(uint64_t));
-        if (p.inject && leader && issued == 0) {
-          // test-only stall: this stage is never armed, so the MMA's wait on it expires
-        } else {
-          uint8_t *sa = tiles + stage * 2 * X_OP;
-          uint8_t *sf = scales + stage * (X_SFA + X_SFB);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * X_STAGE);
+        // test-only stall (inject): the first stage is never armed, so the MMA's wait on it expires
+        if (!(p.inject && leader && issued == 0) && elect_one()) {
+          uint8_t *sa = tiles + stage * C::ops;
+          uint8_t *sf = scales + stage * C::sf;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::stage);
           tma_load_2d_pair(sa, &p.ta, bar, kb * (XK / 2), tl.row0);
-          tma_load_2d_pair(sa + X_OP, &p.tb[rank], bar, kb * (XK / 2), brow);
+          tma_load_2d_pair(sa + X_A, &p.tb[rank], bar, kb * (XK / 2), brow);
           // scale tiles of K tiles 2 kb, 2 kb + 1 (one past an odd end is loaded, not used)
-          tma_load_2d_pair(sf, &p.tsa, bar, 0, tl.row0 / 128 * p.k_tiles + 2 * kb);
-          tma_load_2d_pair(sf + X_SFA, &p.tsb[0], bar, 0, s0 * p.k_tiles + 2 * kb);
-          tma_load_2d_pair(sf + 2 * X_SFA, &p.tsb[1], bar, 0, s1 * p.k_tiles + 2 * kb);
+          tma_load_2d_pair(sf, &p.tsa, bar, 0, sa0 + 2 * kb);
+          tma_load_2d_pair(sf + X_SF, &p.tsb[0], bar, 0, s0 + 2 * kb);
+          if (GLU) tma_load_2d_pair(sf + 2 * X_SF, &p.tsb[1], bar, 0, s0 + 2 * kb);
         }
         ++issued;
         if (++stage == X_STAGES) {
@@ -278,118 +308,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         }
       }
     }
-    if (leader)  // every issued copy (of both CTAs) has landed before exit
+    __syncwarp();
+    if (leader && lane == 0)  // every issued copy (of both CTAs) has landed before exit
       for (long long i = (issued > X_STAGES ? issued - X_STAGES : 0); i < issued; ++i)
         mbar_wait_plain(&full[i % X_STAGES], (uint32_t)((i / X_STAGES) & 1), p.wait_cycles);
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
     // ---------------- scales and MMAs (leader only) ----------------
-    int stage = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    for (int r = 0, t = mx_snake(0, cluster, nclusters); t < total;
-         t = mx_snake(++r, cluster, nclusters)) {
-      if (!mbar_wait(tempty, acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles)) break;
-      tc_fence_after();
-      bool ok = true;
-      for (int kb = 0; kb < k_stages; ++kb) {
-        if (!mbar_wait(&full[stage], phase, p.status, abort_flag, p.wait_cycles)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a = smem_u32(tiles + stage * 2 * X_OP), b = a + X_OP;
-        const uint32_t sf = smem_u32(scales + stage * (X_SFA + X_SFB));
-        const uint32_t ca = tmem_base + X_SF_COL + 32 * stage, cb = ca + 8;
-        const int kt = min(2, p.k_tiles - 2 * kb);  // 128-wide K tiles in this stage
-        for (int j = 0; j < kt; ++j) {
-          tc_cp_scales(ca + 4 * j, sdesc_scales(sf + j * kMx4TileBytes));
-          tc_cp_scales(cb + 8 * j, sdesc_scales(sf + X_SFA + j * kMx4TileBytes));
-          tc_cp_scales(cb + 8 * j + 4, sdesc_scales(sf + 2 * X_SFA + j * kMx4TileBytes));
-        }
-        for (int j = 0; j < kt; ++j) {
+    int tile_count = 0;  // of this cluster
+    for (int r = 0; mx_snake(r, cluster, nclusters) < total; ++r) ++tile_count;
+    const long long n = (long long)tile_count * k_stages;  // stages, of all tiles in a row
+    // scales of the `c`-th stage: its place in the ring, parity and K tile are kept along
+    int cst = 0, ckb = 0;
+    uint32_t cphase = 0;
+    long long copied = 0;
+    auto copy_scales = [&]() {
+      const uint64_t sf = sdesc_scales(smem_u32(scales + cst * C::sf));
+      const uint32_t ca = tmem_base + X_SF_COL + 32 * cst, cb = ca + 8;
+      const int kt = p.k_tiles - 2 * ckb;  // 128-wide K tiles from this stage on
+      if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)  // 64 K (32 bytes, two scales) each
-            tc_mma_mx4(tmem_base, sdesc_kmajor_sw128(a + (2 * j + i) * 32),
-                       sdesc_kmajor_sw128(b + (2 * j + i) * 32), idesc_mx4(2 * XM, XN, 2 * i),
-                       ca + 4 * j, cb + 8 * j, (kb | j | i) != 0 ? 1u : 0u);
-        }
-        tc_commit_pair_mc(&empty[stage]);
-        if (++stage == X_STAGES) {
-          stage = 0;
-          phase ^= 1u;
+        for (int j = 0; j < 2; ++j) {
+          if (j >= kt) break;
+          tc_cp_scales(ca + 4 * j, sf + j * (kMx4TileBytes / 16));
+#pragma unroll
+          for (int q = 0; q < C::sfb; ++q)
+            tc_cp_scales(cb + 4 * C::sfb * j + 4 * q,
+                         sf + ((1 + q) * X_SF + j * kMx4TileBytes) / 16);
         }
       }
-      if (!ok) break;
-      tc_commit_pair_mc(tfull);
-      acc_phase ^= 1u;
+      __syncwarp();
+      ++copied;
+      if (++ckb == k_stages) ckb = 0;
+      if (++cst == X_STAGES) {
+        cst = 0;
+        cphase ^= 1u;
+      }
+    };
+    int stage = 0, acc = 0, kb = 0;
+    uint32_t acc_phase = 0;
+    for (long long i = 0; i < n; ++i) {
+      if (kb == 0) {
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles)) break;
+        tc_fence_after();
+      }
+      if (copied == i) {
+        if (!mbar_wait(&full[cst], cphase, p.status, abort_flag, p.wait_cycles)) break;
+        tc_fence_after();
+        copy_scales();
+      }
+      if (copied < n && __all_sync(0xFFFFFFFFu, mbar_try_wait(&full[cst], cphase))) {  // next stage
+        tc_fence_after();
+        copy_scales();
+      }
+      const uint32_t a = smem_u32(tiles + stage * C::ops);
+      const uint64_t ad = sdesc_kmajor_sw128(a), bd = sdesc_kmajor_sw128(a + X_A);
+      const uint32_t ca = tmem_base + X_SF_COL + 32 * stage, cb = ca + 8;
+      const uint32_t d = tmem_base + (uint32_t)(acc * C::N);
+      const int kt = p.k_tiles - 2 * kb;
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (j >= kt) break;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)  // 64 K (32 bytes, two scales) each
+            tc_mma_mx4(d, ad + 2 * (2 * j + q), bd + 2 * (2 * j + q),
+                       idesc_mx4(2 * XM, C::N, 2 * q), ca + 4 * j, cb + 4 * C::sfb * j,
+                       (kb | j | q) != 0 ? 1u : 0u);
+        }
+        tc_commit_pair_mc(&empty[stage]);
+        if (kb == k_stages - 1) tc_commit_pair_mc(&tfull[acc]);
+      }
+      __syncwarp();
+      if (++stage == X_STAGES) stage = 0;
+      if (++kb == k_stages) {
+        kb = 0;
+        if (++acc == C::nacc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
     }
-    tc_commit_pair(drain);
+    if (elect_one()) tc_commit_pair(drain);
+    __syncwarp();
     mbar_wait_plain(drain, 0, p.wait_cycles);
   } else if (warp >= 2) {
     // ---------------- epilogue (both CTAs) ----------------
-    const int sub = warp & 3;          // tensor-memory lanes of this warp
-    const int half = (warp - 2) >> 2;  // its half of the columns
+    // GLU: 16 warps per tile, a quarter of the columns each.  DOWN: the two halves of the warps
+    // take every second tile (accumulator), half of the columns each.
+    const int sub = warp & 3;  // tensor-memory lanes of this warp
+    const int quarter = (warp - 2) >> 2;
+    const int part = GLU ? quarter : quarter & 1, mine_acc = GLU ? 0 : quarter >> 1;
     const uint32_t box = smem_u32(outbuf) + (uint32_t)((warp - 2) * X_BOX);
     uint32_t acc_phase = 0;
-    for (int r = 0, t = mx_snake(0, cluster, nclusters); t < total;
-         t = mx_snake(++r, cluster, nclusters)) {
+    for (int r = mine_acc, t; (t = mx_snake(r, cluster, nclusters)) < total; r += C::nacc) {
       const MxTile tl = mx_decode(p, t, ustart, rank);
       const int row = tl.row0 + sub * 32 + lane;
       float wr = 0.0f;
       if (!GLU && !tl.dummy)
         wr = bfp_row_weight(p.padded_bins, p.bins, p.indices, p.weights, tl.e, row);
       int good = 1;
-      if (lane == 0) good = mbar_wait(tfull, acc_phase, p.status, abort_flag, p.wait_cycles) ? 1 : 0;
+      if (lane == 0)
+        good = mbar_wait(&tfull[mine_acc], acc_phase, p.status, abort_flag, p.wait_cycles) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, good, 0)) break;
       acc_phase ^= 1u;
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(sub * 32) << 16);
-      uint32_t v0[2][32], v1[2][32];
-      // GLU: 64 gate columns and their 64 up columns; DOWN: 128 columns
-      const int c0 = GLU ? 64 * half : 128 * half, c1 = GLU ? 128 + c0 : c0 + 64;
-      tmem_ld32(tb + c0, v0[0]);
-      tmem_ld32(tb + c0 + 32, v0[1]);
-      tmem_ld32(tb + c1, v1[0]);
-      tmem_ld32(tb + c1 + 32, v1[1]);
+      const uint32_t tb = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(mine_acc * C::N);
+      uint32_t v0[32], v1[32];
+      // GLU: 32 gate columns and their 32 up columns; DOWN: 64 columns
+      const int c0 = (GLU ? 32 : 64) * part, c1 = GLU ? 128 + c0 : c0 + 32;
+      tmem_ld32(tb + c0, v0);
+      tmem_ld32(tb + c1, v1);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_tempty);  // accumulator free: values in registers
+      if (lane == 0)  // accumulator free: values in registers
+        mbar_arrive_cluster(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
       if (tl.dummy) continue;
       if (GLU) {
-        glu_store(p, v0, v1, row, tl.n, half);
+        glu_store(p, v0, v1, row, tl.n * 4 + part);
       } else {
-        const int n0 = tl.n * XN + half * 128;
-        if (n0 >= p.h) continue;
+        const int n0 = tl.n * 128 + part * 64;
         uint32_t mb = 0u;  // largest magnitude, as integers (NaN above inf)
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          mb = max(max(mb, max(v0[0][i] & 0x7FFFFFFFu, v0[1][i] & 0x7FFFFFFFu)),
-                   max(v1[0][i] & 0x7FFFFFFFu, v1[1][i] & 0x7FFFFFFFu));
-        const float m = __uint_as_float(mb);
+        for (int i = 0; i < 32; ++i) mb = max(mb, max(v0[i] & 0x7FFFFFFFu, v1[i] & 0x7FFFFFFFu));
+        // ... of the 128-column group: exchanged with the warp of its other 64 columns
+        uint32_t *mine = reinterpret_cast<uint32_t *>(amax) + (warp - 2) * 32 + lane;
+        uint32_t *other = mine + (part ? -128 : 128);  // four warps on
+        const int bar = 1 + mine_acc * 4 + sub;
+        *mine = mb;
+        asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+        mb = max(mb, *other);
+        asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // read before the next tile's
         float stored;
-        const float k = bfp_scale(m * fabsf(wr), stored) * wr;
-        p.yscale[(size_t)row * dmoe_scale_stride(p.h) + n0 / 128] = stored;
+        const float k = bfp_scale(__uint_as_float(mb) * fabsf(wr), stored) * wr;
+        if (part == 0) p.yscale[(size_t)row * dmoe_scale_stride(p.h) + n0 / 128] = stored;
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        const uint32_t dst = box + (uint32_t)(lane * 128);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {  // 64 columns per box
-          const uint32_t(&v)[2][32] = b ? v1 : v0;
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          const uint32_t dst = box + (uint32_t)(lane * 128);
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t(&v)[32] = c < 4 ? v0 : v1;
+          uint32_t o[4];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[i] = pack_f16x2(__uint_as_float(v[c >> 2][8 * (c & 3) + 2 * i]) * k,
-                                __uint_as_float(v[c >> 2][8 * (c & 3) + 2 * i + 1]) * k);
-            st_shared_v4(dst + (uint32_t)((c ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d_u32(&p.ty, box, n0 + 64 * b, tl.row0 + sub * 32);
-            bulk_commit();
-          }
+          for (int i = 0; i < 4; ++i)
+            o[i] = pack_f16x2(__uint_as_float(v[8 * (c & 3) + 2 * i]) * k,
+                              __uint_as_float(v[8 * (c & 3) + 2 * i + 1]) * k);
+          st_shared_v4(dst + (uint32_t)((c ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d_u32(&p.ty, box, n0, tl.row0 + sub * 32);
+          bulk_commit();
         }
       }
     }
@@ -405,12 +475,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   }
 }
 
-// Elements [rows, cols / 2] bytes: boxes of 128 rows x 128 bytes, 128-byte swizzle.
-bool map_codes(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols) {
+// Elements [rows, cols / 2] bytes: boxes of box_rows x 128 bytes, 128-byte swizzle.
+bool map_codes(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {cols / 2, rows}, strides[1] = {cols / 2};
-  cuuint32_t box[2] = {XK / 2, XM}, estr[2] = {1, 1};
+  cuuint32_t box[2] = {XK / 2, box_rows}, estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -460,12 +530,12 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   static int max_clusters = 0;
   std::call_once(once, [] {
     attr_err = cudaFuncSetAttribute(k_mx4_gemm<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)X_SMEM);
+                                    (int)MxCfg<GLU>::smem);
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
     cfg.blockDim = dim3(X_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = X_SMEM;
+    cfg.dynamicSmemBytes = MxCfg<GLU>::smem;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, k_mx4_gemm<GLU>, &cfg) != cudaSuccess || n < 1)
       n = device_sm_count() / 2;
@@ -474,7 +544,7 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   if (attr_err != cudaSuccess) return attr_err;
   const long long max_tiles = ((long long)g.nblk_cap / 2 + g.E) * p.n_tiles;
   const long long clusters = max_tiles < max_clusters ? max_tiles : max_clusters;
-  return launch_pdl(k_mx4_gemm<GLU>, (int)(2 * clusters), X_THREADS, X_SMEM, st, p);
+  return launch_pdl(k_mx4_gemm<GLU>, (int)(2 * clusters), X_THREADS, MxCfg<GLU>::smem, st, p);
 }
 
 }  // namespace
@@ -485,14 +555,14 @@ cudaError_t launch_mx4_glu(const GemmProblem &g, const void *xq, const void *xs,
   MxParams p;
   memset(&p, 0, sizeof(p));
   const uint64_t P = (uint64_t)g.nblk_cap * XM, EF = (uint64_t)g.E * g.f;
-  if (!map_codes(&p.ta, xq, P, g.h) || !map_scales(&p.tsa, xs, P, g.h) ||
-      !map_codes(&p.tb[0], w1, EF, g.h) || !map_scales(&p.tsb[0], s1, EF, g.h) ||
-      !map_codes(&p.tb[1], w3, EF, g.h) || !map_scales(&p.tsb[1], s3, EF, g.h))
+  if (!map_codes(&p.ta, xq, P, g.h, XM) || !map_scales(&p.tsa, xs, P, g.h) ||
+      !map_codes(&p.tb[0], w1, EF, g.h, 128) || !map_scales(&p.tsb[0], s1, EF, g.h) ||
+      !map_codes(&p.tb[1], w3, EF, g.h, 128) || !map_scales(&p.tsb[1], s3, EF, g.h))
     return cudaErrorInvalidValue;
   p.ty = p.ta;
   p.hq = static_cast<uint8_t *>(hq);
   p.hs = static_cast<uint8_t *>(hs);
-  p.n_tiles = g.f / (XN / 2);
+  p.n_tiles = g.f / 128;
   p.k_tiles = g.h / 128;
   return launch_mx<true>(g, p, st);
 }
@@ -502,14 +572,14 @@ cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs
   MxParams p;
   memset(&p, 0, sizeof(p));
   const uint64_t P = (uint64_t)g.nblk_cap * XM, EH = (uint64_t)g.E * g.h;
-  if (!map_codes(&p.ta, hq, P, g.f) || !map_scales(&p.tsa, hs, P, g.f) ||
-      !map_codes(&p.tb[0], w2, EH, g.f) || !map_scales(&p.tsb[0], s2, EH, g.f) ||
+  if (!map_codes(&p.ta, hq, P, g.f, XM) || !map_scales(&p.tsa, hs, P, g.f) ||
+      !map_codes(&p.tb[0], w2, EH, g.f, 64) || !map_scales(&p.tsb[0], s2, EH, g.f) ||
       !map_rows16(&p.ty, y_pad, P, g.h))
     return cudaErrorInvalidValue;
   p.tb[1] = p.tb[0];
   p.tsb[1] = p.tsb[0];
   p.yscale = y_scale;
-  p.n_tiles = (g.h + XN - 1) / XN;
+  p.n_tiles = g.h / 128;
   p.k_tiles = g.f / 128;
   return launch_mx<false>(g, p, st);
 }
