@@ -81,15 +81,4 @@ __device__ __forceinline__ float bfp_scale(float m, float &stored) {
   return __uint_as_float((uint32_t)(127 + es) << 23);
 }
 
-// Routing weight of padded row `row` of expert e (0 for a padding row).
-__device__ __forceinline__ float bfp_row_weight(const int32_t *padded_bins, const int32_t *bins,
-                                                const int32_t *indices, const float *weights,
-                                                int e, int row) {
-  const int pstart = (e > 0) ? __ldg(padded_bins + e - 1) : 0;
-  const int bstart = (e > 0) ? __ldg(bins + e - 1) : 0;
-  const int local = row - pstart;
-  return (local < __ldg(bins + e) - bstart) ? __ldg(weights + __ldg(indices + bstart + local))
-                                            : 0.0f;
-}
-
 }  // namespace dmoe

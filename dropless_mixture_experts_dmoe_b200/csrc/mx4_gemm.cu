@@ -61,8 +61,10 @@ struct MxCfg {
   static constexpr int stages = GLU ? 6 : 5;
   static constexpr int out = GLU ? 0 : X_EPI * X_BOX;
   static constexpr int amax = GLU ? 0 : X_EPI * 32 * 4;
+  // per expert: first unit and first row block (GLU, DOWN), first entry (DOWN)
+  static constexpr int tables = GLU ? 2 : 3;
   static constexpr size_t smem = 1024 + (size_t)stages * stage + out + amax + 256 +
-                                 sizeof(int) * (DMOE_MAX_EXPERTS + 1);
+                                 sizeof(int) * tables * (DMOE_MAX_EXPERTS + 1);
   // arrivals that release an accumulator: the epilogue warps of both CTAs that read it
   static constexpr int epi_arrivals = 2 * X_EPI / nacc;
   static_assert(X_SF_COL + 32 * stages <= X_TMEM, "tensor memory");
@@ -90,30 +92,36 @@ struct MxTile {
   bool dummy;
 };
 
+// The schedule's tables in shared memory, [E + 1] each: units and row blocks before expert e.
+struct MxTables {
+  const int *ustart, *bstart;
+};
+
 // Tile t -> expert, column tile, this CTA's rows; units of an expert in chunks of p.group, the
 // unit varying fastest so that concurrent pairs share B.
-__device__ __forceinline__ MxTile mx_decode(const MxParams &p, int t, const int *ustart,
+__device__ __forceinline__ MxTile mx_decode(const MxParams &p, int t, const MxTables &tb,
                                             uint32_t rank) {
+  // the expert whose units hold vu = t / n_tiles, the last one with ustart[e] <= vu: the whole
+  // warp looks, first at every 32nd expert, then at the 32 from there on
+  const int lane = threadIdx.x & 31;
   const int vu = t / p.n_tiles;
-  int lo = 0, hi = p.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ustart[mid] <= vu)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int g = 32 * lane, e0 =
+      32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < p.E && tb.ustart[min(g, p.E)] <= vu)) - 1);
+  const int c = e0 + lane, lo =
+      e0 + __popc(__ballot_sync(0xFFFFFFFFu, c < p.E && tb.ustart[min(c, p.E)] <= vu)) - 1;
+  const int u0 = tb.ustart[lo], units = tb.ustart[lo + 1] - u0;
+  int c0 = 0, cs = max(units, 1);  // (no units at all: nothing of the result is used)
+  if (units > p.group) {
+    c0 = ((vu - u0) / p.group) * p.group;
+    cs = min(p.group, units - c0);
   }
-  const int units = ustart[lo + 1] - ustart[lo];
-  const int c0 = ((vu - ustart[lo]) / p.group) * p.group;
-  const int cs = min(p.group, units - c0);
-  const int lt = t - (ustart[lo] + c0) * p.n_tiles;
+  const int lt = t - (u0 + c0) * p.n_tiles;
   MxTile tl;
   tl.e = lo;
   tl.n = lt / cs;
   const int unit = c0 + (lt - tl.n * cs);
-  const int first = ((lo > 0) ? p.padded_bins[lo - 1] : 0) / XM;
-  const int b = first + 2 * unit + (int)rank;
-  tl.dummy = b >= p.padded_bins[lo] / XM;
+  const int b = tb.bstart[lo] + 2 * unit + (int)rank;
+  tl.dummy = b >= tb.bstart[lo + 1];
   tl.row0 = (tl.dummy ? p.nblk_cap : b) * XM;  // past the last row: loads read zeros
   return tl;
 }
@@ -150,6 +158,13 @@ __device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// Arrival on a barrier of the pair's leader that hands over nothing but tensor memory already
+// read (tcgen05.wait::ld and the fence come before it).  A cluster-scope release here would
+// wait for this thread's earlier global stores: it took over 1000 clocks a tile.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // One lane of a converged warp.  The producer and MMA warps run their loops as whole warps and
 // elect the lane only around the instructions: their operands then stay in uniform registers
 // (a loop of one lane moved every operand over, about 90 clocks an instruction).
@@ -158,6 +173,18 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(p));
   return p != 0;
+}
+
+// Whether the phase has completed, without waiting (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ int mx_snake(int r, int cluster, int nclusters) {
@@ -213,7 +240,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   float *amax = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bars) + 256);
-  int *ustart = reinterpret_cast<int *>(amax + MxCfg<GLU>::amax / 4);  // [E + 1]
+  int *ustart = reinterpret_cast<int *>(amax + MxCfg<GLU>::amax / 4);
+  int *bstart = ustart + p.E + 1, *estart = bstart + p.E + 1;  // [E + 1] each
+  const MxTables tables{ustart, bstart};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -240,8 +269,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   }
   pdl_wait();  // the next kernel is released as this grid's CTAs exit
   for (int e = threadIdx.x; e < p.E; e += X_THREADS) {
-    const int blocks = (p.padded_bins[e] - ((e > 0) ? p.padded_bins[e - 1] : 0)) / XM;
-    ustart[e + 1] = (blocks + 1) / 2;
+    const int end = p.padded_bins[e] / XM, first = (e > 0) ? p.padded_bins[e - 1] / XM : 0;
+    ustart[e + 1] = (end - first + 1) / 2;
+    bstart[e + 1] = end;
+    if (!GLU) estart[e + 1] = p.bins[e];
+  }
+  if (threadIdx.x == 0) {
+    bstart[0] = 0;
+    if (!GLU) estart[0] = 0;
   }
   __syncthreads();
   if (warp == 0) {
@@ -276,9 +311,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    for (int r = 0, t = mx_snake(0, cluster, nclusters); ok && t < total;
-         t = mx_snake(++r, cluster, nclusters)) {
-      const MxTile tl = mx_decode(p, t, ustart, rank);
+    int t = mx_snake(0, cluster, nclusters);
+    MxTile tl = mx_decode(p, max(0, min(t, total - 1)), tables, rank), nx = tl;
+    for (int r = 0; ok && t < total; tl = nx) {
+      // the next tile is looked up once this one's first stage is on its way
+      const int tn = mx_snake(++r, cluster, nclusters);
       // B rows: this CTA's half; scale row tiles of all of B
       const int brow =
           GLU ? tl.e * p.f + tl.n * 128 : tl.e * p.h + tl.n * 128 + (int)rank * 64;
@@ -301,12 +338,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
           tma_load_2d_pair(sf + X_SF, &p.tsb[0], bar, 0, s0 + 2 * kb);
           if (GLU) tma_load_2d_pair(sf + 2 * X_SF, &p.tsb[1], bar, 0, s0 + 2 * kb);
         }
+        if (kb == 0 && tn < total) nx = mx_decode(p, tn, tables, rank);
         ++issued;
         if (++stage == X_STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
+      t = tn;
     }
     __syncwarp();
     if (leader && lane == 0)  // every issued copy (of both CTAs) has landed before exit
@@ -356,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         tc_fence_after();
         copy_scales();
       }
-      if (copied < n && __all_sync(0xFFFFFFFFu, mbar_try_wait(&full[cst], cphase))) {  // next stage
+      if (copied < n && __all_sync(0xFFFFFFFFu, mbar_test(&full[cst], cphase))) {  // next stage
         tc_fence_after();
         copy_scales();
       }
@@ -399,13 +438,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     const int quarter = (warp - 2) >> 2;
     const int part = GLU ? quarter : quarter & 1, mine_acc = GLU ? 0 : quarter >> 1;
     const uint32_t box = smem_u32(outbuf) + (uint32_t)((warp - 2) * X_BOX);
+    // a tile's rows, and the routing weight of this thread's row, are looked up while the tile
+    // before it is converted and stored (the weight is two dependent loads)
+    auto weight_of = [&](const MxTile &tl) -> float {
+      if (GLU || tl.dummy) return 0.0f;
+      const int local = tl.row0 + sub * 32 + lane - bstart[tl.e] * XM, first = estart[tl.e];
+      return (local < estart[tl.e + 1] - first) ? __ldg(p.weights + __ldg(p.indices + first + local))
+                                                : 0.0f;  // a padding row
+    };
     uint32_t acc_phase = 0;
-    for (int r = mine_acc, t; (t = mx_snake(r, cluster, nclusters)) < total; r += C::nacc) {
-      const MxTile tl = mx_decode(p, t, ustart, rank);
+    int r = mine_acc, t = mx_snake(r, cluster, nclusters);
+    MxTile nx = mx_decode(p, max(0, min(t, total - 1)), tables, rank);
+    float wnx = (t < total) ? weight_of(nx) : 0.0f;
+    while (t < total) {
+      const MxTile tl = nx;
+      const float wr = wnx;
       const int row = tl.row0 + sub * 32 + lane;
-      float wr = 0.0f;
-      if (!GLU && !tl.dummy)
-        wr = bfp_row_weight(p.padded_bins, p.bins, p.indices, p.weights, tl.e, row);
       int good = 1;
       if (lane == 0)
         good = mbar_wait(&tfull[mine_acc], acc_phase, p.status, abort_flag, p.wait_cycles) ? 1 : 0;
@@ -422,7 +470,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0)  // accumulator free: values in registers
-        mbar_arrive_cluster(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
+        mbar_arrive_remote(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
+      r += C::nacc;
+      t = mx_snake(r, cluster, nclusters);
+      if (t < total) {
+        nx = mx_decode(p, t, tables, rank);
+        wnx = weight_of(nx);
+      }
       if (tl.dummy) continue;
       if (GLU) {
         glu_store(p, v0, v1, row, tl.n * 4 + part);
