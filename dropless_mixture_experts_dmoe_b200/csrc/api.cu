@@ -304,9 +304,10 @@ int forward_few(const dmoe_dims *dims, const void *x, const void *logits, FewWei
 }
 
 // 4-bit forward workspace: X_pad codes [P, h/2] | its scales [P*h/32] | H codes [P, f/2] | its
-// scales [P*f/32] | Y_pad [P,h] fp16 | Y_pad scales [P, dmoe_scale_stride(h)] fp32
+// scales [P*f/32] | Y_pad [P,h] fp16 | Y_pad scales [P, dmoe_scale_stride(h)] fp32 | routing weight
+// of each row [P] fp32
 struct Mx4Layout {
-  size_t xq, xs, hq, hs, ypad, yscale, total;
+  size_t xq, xs, hq, hs, ypad, yscale, wrow, total;
 };
 Mx4Layout mx4_layout(const dmoe_dims *d) {
   const size_t P = (size_t)pmax_of(d);
@@ -317,7 +318,8 @@ Mx4Layout mx4_layout(const dmoe_dims *d) {
   l.hs = align_up(l.hq + P * d->ffn / 2);
   l.ypad = align_up(l.hs + P * d->ffn / 32);
   l.yscale = align_up(l.ypad + P * d->hidden * 2);
-  l.total = align_up(l.yscale + P * scale_cols(d) * sizeof(float));
+  l.wrow = align_up(l.yscale + P * scale_cols(d) * sizeof(float));
+  l.total = align_up(l.wrow + P * sizeof(float));
   return l;
 }
 
@@ -780,16 +782,18 @@ int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t *w = static_cast<uint8_t *>(ws);
   float *yscale = reinterpret_cast<float *>(w + l.yscale);
+  float *wrow = reinterpret_cast<float *>(w + l.wrow);
   if ((rc = launch_rc(launch_mx4_gather(dims->T, dims->hidden, dims->top_k, dims->num_experts, x,
                                         map->dest_row, map->tokens_per_expert, map->padded_bins,
-                                        w + l.xq, w + l.xs, st, entry_offsets_of(dims, map)))))
+                                        w + l.xq, w + l.xs, st, entry_offsets_of(dims, map),
+                                        map->weights, wrow))))
     return rc;
   const GemmProblem g = problem_of(dims, map);
   if ((rc = launch_rc(launch_mx4_glu(g, w + l.xq, w + l.xs, w1->codes, w1->scales, w3->codes,
                                      w3->scales, w + l.hq, w + l.hs, st))))
     return rc;
-  if ((rc = launch_rc(launch_mx4_down(g, w + l.hq, w + l.hs, w2->codes, w2->scales, w + l.ypad,
-                                      yscale, st))))
+  if ((rc = launch_rc(launch_mx4_down(g, w + l.hq, w + l.hs, w2->codes, w2->scales, wrow,
+                                      w + l.ypad, yscale, st))))
     return rc;
   return dmoe_padded_scatter(dims, w + l.ypad, yscale, map, nullptr, y, stream);  // rows weighted
 }

@@ -196,14 +196,17 @@ cudaError_t launch_mx4_dequantize(long long rows, long long cols, const void *co
                                   const void *scales, void *dst, cudaStream_t st);
 cudaError_t launch_mx4_gather(int T, int h, int k, int E, const void *x, const int32_t *dest_row,
                               const int32_t *counts, const int32_t *padded_bins, void *codes,
-                              void *scales, cudaStream_t st, const int32_t *offsets);
+                              void *scales, cudaStream_t st, const int32_t *offsets,
+                              const float *weights, float *row_weight);
 // GLU: X_pad in the format -> H [P_max, f] in the format (converted from fp32).  DOWN: H in the
 // format -> Y_pad in block floating point, rows weighted (as launch_down_gemm).
 cudaError_t launch_mx4_glu(const GemmProblem &g, const void *xq, const void *xs, const void *w1,
                            const void *s1, const void *w3, const void *s3, void *hq, void *hs,
                            cudaStream_t st);
+// row_weight: [P_max] the routing weight of each padded row, 0 for a padding row.
 cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs, const void *w2,
-                            const void *s2, void *y_pad, float *y_scale, cudaStream_t st);
+                            const void *s2, const float *row_weight, void *y_pad, float *y_scale,
+                            cudaStream_t st);
 
 int device_sm_count();
 

@@ -134,13 +134,14 @@ __global__ void __launch_bounds__(kMx4Threads)
 }
 
 // The padded gather with the conversion in it: a warp converts up to 1024 columns of a token row
-// once, all its loads in flight, and writes them to the token's padded rows; padding rows get
-// elements and scales of zero.
+// once, all its loads in flight, and writes them to the token's padded rows, with each row's
+// routing weight beside; padding rows get elements, scales and a weight of zero.
 __global__ void __launch_bounds__(kMx4Threads)
     k_mx4_gather(int T, int h, int k, int E, const uint4 *__restrict__ x,
                  const int32_t *__restrict__ dest_row, const int32_t *__restrict__ counts,
                  const int32_t *__restrict__ padded_bins, uint32_t *__restrict__ codes,
-                 uint8_t *__restrict__ scales, const int32_t *__restrict__ offsets) {
+                 uint8_t *__restrict__ scales, const int32_t *__restrict__ offsets,
+                 const float *__restrict__ weights, float *__restrict__ row_weight) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kMx4Threads)
       for (int c0 = 0; c0 < cnt; c0 += 32) {
         const int nc = min(32, cnt - c0);
         const int d = (lane < nc) ? __ldg(dest_row + base + c0 + lane) : -1;
+        if (v0 < 32 && d >= 0) row_weight[d] = __ldg(weights + base + c0 + lane);  // first slice
         for (int s = 0; s < nc; ++s) {
           const int r = __shfl_sync(0xFFFFFFFFu, d, s);
           if (r < 0) continue;
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(kMx4Threads)
       const int e = (int)(p / kBlock), r = (int)(p % kBlock);
       const int row = ((e > 0) ? padded_bins[e - 1] : 0) + counts[e] + r;
       if (row >= padded_bins[e]) continue;
+      if (lane == 0) row_weight[row] = 0.0f;
       for (int v = lane; v < vpr; v += 32) {
         codes[(size_t)row * vpr + v] = 0u;
         if ((v & 15) == 0)
@@ -225,11 +228,13 @@ cudaError_t launch_mx4_dequantize(long long rows, long long cols, const void *co
 
 cudaError_t launch_mx4_gather(int T, int h, int k, int E, const void *x, const int32_t *dest_row,
                               const int32_t *counts, const int32_t *padded_bins, void *codes,
-                              void *scales, cudaStream_t st, const int32_t *offsets) {
+                              void *scales, cudaStream_t st, const int32_t *offsets,
+                              const float *weights, float *row_weight) {
   const long long items = (long long)T * ((h / 8 + 127) / 128) + (long long)kBlock * E;
   return launch_pdl(k_mx4_gather, mx4_grid(items, kMx4Warps), kMx4Threads, 0, st, T, h, k, E,
                     static_cast<const uint4 *>(x), dest_row, counts, padded_bins,
-                    static_cast<uint32_t *>(codes), static_cast<uint8_t *>(scales), offsets);
+                    static_cast<uint32_t *>(codes), static_cast<uint8_t *>(scales), offsets, weights,
+                    row_weight);
 }
 
 }  // namespace dmoe

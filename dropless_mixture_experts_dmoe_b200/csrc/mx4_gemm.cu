@@ -61,8 +61,7 @@ struct MxCfg {
   static constexpr int stages = GLU ? 6 : 5;
   static constexpr int out = GLU ? 0 : X_EPI * X_BOX;
   static constexpr int amax = GLU ? 0 : X_EPI * 32 * 4;
-  // per expert: first unit and first row block (GLU, DOWN), first entry (DOWN)
-  static constexpr int tables = GLU ? 2 : 3;
+  static constexpr int tables = 2;  // per expert: units and row blocks before it
   static constexpr size_t smem = 1024 + (size_t)stages * stage + out + amax + 256 +
                                  sizeof(int) * tables * (DMOE_MAX_EXPERTS + 1);
   // arrivals that release an accumulator: the epilogue warps of both CTAs that read it
@@ -75,10 +74,11 @@ struct MxParams {
   CUtensorMap ta, tsa;            // A elements and scales
   CUtensorMap tb[2], tsb[2];      // B of the leader's / the peer's half: W1 / W3, or W2 twice
   CUtensorMap ty;                 // DOWN: Y_pad
-  const int32_t *padded_bins, *bins, *indices;
-  const float *weights;
+  const int32_t *padded_bins;
+  const float *row_weight;  // DOWN: [P_max] routing weight of each padded row
   int E, h, f;
   int n_tiles, k_tiles;  // column tiles per unit; 128-wide K tiles
+  uint32_t n_magic;      // ceil(2^32 / n_tiles), or 0
   int nblk_cap, group;
   int inject;
   long long wait_cycles;
@@ -104,7 +104,8 @@ __device__ __forceinline__ MxTile mx_decode(const MxParams &p, int t, const MxTa
   // the expert whose units hold vu = t / n_tiles, the last one with ustart[e] <= vu: the whole
   // warp looks, first at every 32nd expert, then at the 32 from there on
   const int lane = threadIdx.x & 31;
-  const int vu = t / p.n_tiles;
+  // the tile counts divide by a multiplication: the host checked that it is exact for every t
+  const int vu = p.n_magic ? (int)__umulhi((uint32_t)t, p.n_magic) : t / p.n_tiles;
   const int g = 32 * lane, e0 =
       32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < p.E && tb.ustart[min(g, p.E)] <= vu)) - 1);
   const int c = e0 + lane, lo =
@@ -118,7 +119,8 @@ __device__ __forceinline__ MxTile mx_decode(const MxParams &p, int t, const MxTa
   const int lt = t - (u0 + c0) * p.n_tiles;
   MxTile tl;
   tl.e = lo;
-  tl.n = lt / cs;
+  // lt < group * n_tiles: small enough for the nearest float quotient of lt + 1/2 to truncate right
+  tl.n = (lt < (1 << 20)) ? (int)__fdividef((float)lt + 0.5f, (float)cs) : lt / cs;
   const int unit = c0 + (lt - tl.n * cs);
   const int b = tb.bstart[lo] + 2 * unit + (int)rank;
   tl.dummy = b >= tb.bstart[lo + 1];
@@ -175,18 +177,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Whether the phase has completed, without waiting (try_wait may suspend the thread for a while).
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 __device__ __forceinline__ int mx_snake(int r, int cluster, int nclusters) {
   return r * nclusters + ((r & 1) ? nclusters - 1 - cluster : cluster);
 }
@@ -241,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   float *amax = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bars) + 256);
   int *ustart = reinterpret_cast<int *>(amax + MxCfg<GLU>::amax / 4);
-  int *bstart = ustart + p.E + 1, *estart = bstart + p.E + 1;  // [E + 1] each
+  int *bstart = ustart + p.E + 1;  // [E + 1] each
   const MxTables tables{ustart, bstart};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,12 +262,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     const int end = p.padded_bins[e] / XM, first = (e > 0) ? p.padded_bins[e - 1] / XM : 0;
     ustart[e + 1] = (end - first + 1) / 2;
     bstart[e + 1] = end;
-    if (!GLU) estart[e + 1] = p.bins[e];
   }
-  if (threadIdx.x == 0) {
-    bstart[0] = 0;
-    if (!GLU) estart[0] = 0;
-  }
+  if (threadIdx.x == 0) bstart[0] = 0;
   __syncthreads();
   if (warp == 0) {
     int carry = 0;
@@ -353,77 +339,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         mbar_wait_plain(&full[i % X_STAGES], (uint32_t)((i / X_STAGES) & 1), p.wait_cycles);
   } else if (warp == 1 && leader) {
     // ---------------- scales and MMAs (leader only) ----------------
-    int tile_count = 0;  // of this cluster
-    for (int r = 0; mx_snake(r, cluster, nclusters) < total; ++r) ++tile_count;
-    const long long n = (long long)tile_count * k_stages;  // stages, of all tiles in a row
-    // scales of the `c`-th stage: its place in the ring, parity and K tile are kept along
-    int cst = 0, ckb = 0;
-    uint32_t cphase = 0;
-    long long copied = 0;
-    auto copy_scales = [&]() {
-      const uint64_t sf = sdesc_scales(smem_u32(scales + cst * C::sf));
-      const uint32_t ca = tmem_base + X_SF_COL + 32 * cst, cb = ca + 8;
-      const int kt = p.k_tiles - 2 * ckb;  // 128-wide K tiles from this stage on
+    int n = 0;  // stages of this cluster, over all of its tiles
+    for (int r = 0; mx_snake(r, cluster, nclusters) < total; ++r) n += k_stages;
+    // the stage being multiplied, and the next one, whose scales are copied ahead
+    int stage = 0, kb = 0, acc = 0, nstage = 0, nkb = 0;
+    uint32_t acc_phase = 0, nphase = 0;
+    bool ok = true;
+    for (int i = -1; ok && i < n; ++i) {  // i = -1: only the first stage's scales
+      if (i >= 0 && kb == 0)
+        ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles);
+      if (ok && i + 1 < n)
+        ok = mbar_wait(&full[nstage], nphase, p.status, abort_flag, p.wait_cycles);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
       if (elect_one()) {
+        if (i + 1 < n) {
+          const uint64_t sf = sdesc_scales(smem_u32(scales) + nstage * C::sf);
+          const uint32_t ca = tmem_base + X_SF_COL + 32 * nstage, cb = ca + 8;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j >= kt) break;
-          tc_cp_scales(ca + 4 * j, sf + j * (kMx4TileBytes / 16));
+          for (int j = 0; j < 2; ++j) {  // 128-wide K tiles; the last stage may have one
+            if (2 * nkb + j >= p.k_tiles) break;
+            tc_cp_scales(ca + 4 * j, sf + j * (kMx4TileBytes / 16));
 #pragma unroll
-          for (int q = 0; q < C::sfb; ++q)
-            tc_cp_scales(cb + 4 * C::sfb * j + 4 * q,
-                         sf + ((1 + q) * X_SF + j * kMx4TileBytes) / 16);
+            for (int q = 0; q < C::sfb; ++q)
+              tc_cp_scales(cb + 4 * C::sfb * j + 4 * q,
+                           sf + ((1 + q) * X_SF + j * kMx4TileBytes) / 16);
+          }
+        }
+        if (i >= 0) {
+          const uint64_t ad = sdesc_kmajor_sw128(smem_u32(tiles) + stage * C::ops);
+          const uint64_t bd = ad + X_A / 16;
+          const uint32_t ca = tmem_base + X_SF_COL + 32 * stage, cb = ca + 8;
+          const uint32_t d = tmem_base + (uint32_t)(acc * C::N);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (2 * kb + j >= p.k_tiles) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)  // 64 K (32 bytes, two scales) each
+              tc_mma_mx4(d, ad + 2 * (2 * j + q), bd + 2 * (2 * j + q),
+                         idesc_mx4(2 * XM, C::N, 2 * q), ca + 4 * j, cb + 4 * C::sfb * j,
+                         (kb | j | q) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_mc(&empty[stage]);
+          if (kb == k_stages - 1) tc_commit_pair_mc(&tfull[acc]);
         }
       }
       __syncwarp();
-      ++copied;
-      if (++ckb == k_stages) ckb = 0;
-      if (++cst == X_STAGES) {
-        cst = 0;
-        cphase ^= 1u;
-      }
-    };
-    int stage = 0, acc = 0, kb = 0;
-    uint32_t acc_phase = 0;
-    for (long long i = 0; i < n; ++i) {
-      if (kb == 0) {
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles)) break;
-        tc_fence_after();
-      }
-      if (copied == i) {
-        if (!mbar_wait(&full[cst], cphase, p.status, abort_flag, p.wait_cycles)) break;
-        tc_fence_after();
-        copy_scales();
-      }
-      if (copied < n && __all_sync(0xFFFFFFFFu, mbar_test(&full[cst], cphase))) {  // next stage
-        tc_fence_after();
-        copy_scales();
-      }
-      const uint32_t a = smem_u32(tiles + stage * C::ops);
-      const uint64_t ad = sdesc_kmajor_sw128(a), bd = sdesc_kmajor_sw128(a + X_A);
-      const uint32_t ca = tmem_base + X_SF_COL + 32 * stage, cb = ca + 8;
-      const uint32_t d = tmem_base + (uint32_t)(acc * C::N);
-      const int kt = p.k_tiles - 2 * kb;
-      if (elect_one()) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j >= kt) break;
-#pragma unroll
-          for (int q = 0; q < 2; ++q)  // 64 K (32 bytes, two scales) each
-            tc_mma_mx4(d, ad + 2 * (2 * j + q), bd + 2 * (2 * j + q),
-                       idesc_mx4(2 * XM, C::N, 2 * q), ca + 4 * j, cb + 4 * C::sfb * j,
-                       (kb | j | q) != 0 ? 1u : 0u);
+      if (i >= 0) {
+        if (++stage == X_STAGES) stage = 0;
+        if (++kb == k_stages) {
+          kb = 0;
+          if (++acc == C::nacc) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
         }
-        tc_commit_pair_mc(&empty[stage]);
-        if (kb == k_stages - 1) tc_commit_pair_mc(&tfull[acc]);
       }
-      __syncwarp();
-      if (++stage == X_STAGES) stage = 0;
-      if (++kb == k_stages) {
-        kb = 0;
-        if (++acc == C::nacc) {
-          acc = 0;
-          acc_phase ^= 1u;
+      if (i + 1 < n) {
+        if (++nkb == k_stages) nkb = 0;
+        if (++nstage == X_STAGES) {
+          nstage = 0;
+          nphase ^= 1u;
         }
       }
     }
@@ -439,12 +415,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     const int part = GLU ? quarter : quarter & 1, mine_acc = GLU ? 0 : quarter >> 1;
     const uint32_t box = smem_u32(outbuf) + (uint32_t)((warp - 2) * X_BOX);
     // a tile's rows, and the routing weight of this thread's row, are looked up while the tile
-    // before it is converted and stored (the weight is two dependent loads)
+    // before it is converted and stored
     auto weight_of = [&](const MxTile &tl) -> float {
-      if (GLU || tl.dummy) return 0.0f;
-      const int local = tl.row0 + sub * 32 + lane - bstart[tl.e] * XM, first = estart[tl.e];
-      return (local < estart[tl.e + 1] - first) ? __ldg(p.weights + __ldg(p.indices + first + local))
-                                                : 0.0f;  // a padding row
+      return (GLU || tl.dummy) ? 0.0f : __ldg(p.row_weight + tl.row0 + sub * 32 + lane);
     };
     uint32_t acc_phase = 0;
     int r = mine_acc, t = mx_snake(r, cluster, nclusters);
@@ -565,9 +538,6 @@ bool map_rows16(CUtensorMap *m, void *ptr, uint64_t rows, uint64_t cols) {
 template <bool GLU>
 cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   p.padded_bins = g.padded_bins;
-  p.bins = g.bins;
-  p.indices = g.indices;
-  p.weights = g.weights;
   p.E = g.E;
   p.h = g.h;
   p.f = g.f;
@@ -597,6 +567,10 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   });
   if (attr_err != cudaSuccess) return attr_err;
   const long long max_tiles = ((long long)g.nblk_cap / 2 + g.E) * p.n_tiles;
+  // t * ceil(2^32 / n) / 2^32 truncates to t / n while t * n < 2^32
+  p.n_magic = (p.n_tiles > 1 && max_tiles * p.n_tiles < (1LL << 32))
+                  ? (uint32_t)(((1ull << 32) + p.n_tiles - 1) / p.n_tiles)
+                  : 0u;
   const long long clusters = max_tiles < max_clusters ? max_tiles : max_clusters;
   return launch_pdl(k_mx4_gemm<GLU>, (int)(2 * clusters), X_THREADS, MxCfg<GLU>::smem, st, p);
 }
@@ -622,9 +596,11 @@ cudaError_t launch_mx4_glu(const GemmProblem &g, const void *xq, const void *xs,
 }
 
 cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs, const void *w2,
-                            const void *s2, void *y_pad, float *y_scale, cudaStream_t st) {
+                            const void *s2, const float *row_weight, void *y_pad, float *y_scale,
+                            cudaStream_t st) {
   MxParams p;
   memset(&p, 0, sizeof(p));
+  p.row_weight = row_weight;
   const uint64_t P = (uint64_t)g.nblk_cap * XM, EH = (uint64_t)g.E * g.h;
   if (!map_codes(&p.ta, hq, P, g.f, XM) || !map_scales(&p.tsa, hs, P, g.f) ||
       !map_codes(&p.tb[0], w2, EH, g.f, 64) || !map_scales(&p.tsb[0], s2, EH, g.f) ||
