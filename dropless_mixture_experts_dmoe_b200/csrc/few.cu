@@ -170,6 +170,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
+// 16 bytes, past L1.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on bar when all of this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int x, int y, int z) {
   asm volatile(
@@ -240,6 +249,7 @@ struct FewCfg {
   // a multiple of 128 keeps the reads free of bank conflicts
   static constexpr int x_row = CH * 2 + (MX4 ? 64 : 16);
   static constexpr int x_bytes = BR * 8 * NT * x_row;
+  static constexpr bool xbulk = CH * 2 >= 512;
   static constexpr int sb_row = CH / 8 + 16;  // a token's block scales
   static constexpr int sb_bytes = SB ? 8 * NT * sb_row : 0;
   static constexpr int o_sc = w_bytes, o_x = o_sc + mats * sc_mat, o_sb = o_x + x_bytes;
@@ -258,20 +268,22 @@ struct FewCfg {
   static_assert(2 * P * 8 <= 112, "barriers");
 };
 
-// Bytes of the expert lists: entries [n] (j | token << 16), starts [E + 1], experts in use
+// Bytes of the expert lists: entries [n] (j | token << 16), a factor of each [n] (DOWN: its
+// weight; GLU with 4-bit weights: the scale of its token's x), starts [E + 1], experts in use
 // (uint16).
 __host__ __device__ inline size_t few_list_bytes(int E, int n) {
-  const size_t a = (size_t)n * 4 + (size_t)(E + 1) * 4 + (size_t)(E < n ? E : n) * 2;
+  const size_t a = (size_t)n * 8 + (size_t)(E + 1) * 4 + (size_t)(E < n ? E : n) * 2;
   return (a + 15) / 16 * 16;
 }
 
 struct FewLists {
   uint32_t *ent;
+  float *fac;
   int *start;
   uint16_t *act;
   __device__ __forceinline__ FewLists(uint8_t *base, int E, int n)
-      : ent(reinterpret_cast<uint32_t *>(base)), start(reinterpret_cast<int *>(ent + n)),
-        act(reinterpret_cast<uint16_t *>(start + E + 1)) {}
+      : ent(reinterpret_cast<uint32_t *>(base)), fac(reinterpret_cast<float *>(ent + n)),
+        start(reinterpret_cast<int *>(fac + n)), act(reinterpret_cast<uint16_t *>(start + E + 1)) {}
 };
 
 // Expert of entry j, or -1 for one that is not listed: an id outside [0, E), or an expert that an
@@ -288,18 +300,19 @@ __device__ __forceinline__ int few_entry(const FewParams &p, int j) {
 
 // Weight of expert e for the token of its listed entry j.
 __device__ __forceinline__ float few_weight(const FewParams &p, int j, int e) {
-  float w = __ldg(p.weights + j);
+  float w = __ldcg(p.weights + j);
   if (p.given)
     for (int i = j + 1; i < j - j % p.k + p.k; ++i)
-      if (__ldg(p.top + i) == e) w += __ldg(p.weights + i);
+      if (__ldcg(p.top + i) == e) w += __ldcg(p.weights + i);
   return w;
 }
 
 // The experts in use, in increasing order, and their entries: start[e] .. start[e + 1] in ent.
 // Returns the number of experts in use.  An entry's place in its expert's list decides only
 // which column of the product it is, so the order the atomics give does not show in any result.
-template <int THREADS>
+template <class C>
 __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, int *s_act) {
+  constexpr int THREADS = C::threads;
   const int n = p.T * p.k, lane = threadIdx.x & 31;
   int *start = l.start;
   for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = 0;
@@ -334,7 +347,14 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
     const int e = few_entry(p, j);
-    if (e >= 0) l.ent[atomicSub(&start[e], 1) - 1] = (uint32_t)j | ((uint32_t)(j / p.k) << 16);
+    if (e < 0) continue;
+    const int at = atomicSub(&start[e], 1) - 1, t = j / p.k;
+    l.ent[at] = (uint32_t)j | ((uint32_t)t << 16);
+    // 4-bit products come out halved (see blocks())
+    if (C::DOWN)
+      l.fac[at] = few_weight(p, j, e) * (C::MX4 ? 0.5f : 1.0f);
+    else if (C::MX4)
+      l.fac[at] = 0.5f * __ldcg(p.xscale + t);
   }
   __syncthreads();  // start[e] is now the first entry of e
   return *s_act;
@@ -401,10 +421,10 @@ struct FewKernel {
   __device__ __forceinline__ int width(const FewPos &q) const {
     return min(C::CH, K - q.chunk * C::CH);
   }
-  __device__ __forceinline__ uint32_t bytes(const FewPos &q) const {
+  __device__ __forceinline__ uint32_t bytes(const FewPos &q) const {  // that bulk copies bring
     const uint32_t w = width(q), nr = min(q.cnt, 8 * C::NT);
     return C::w_bytes + (C::MX4 ? C::mats * (w >> 7) * kMx4TileBytes : 0) +
-           nr * (C::BR * w * 2 + (C::SB ? w >> 3 : 0));
+           (C::xbulk ? nr * (C::BR * w * 2 + (C::SB ? w >> 3 : 0)) : 0);
   }
   // Weights and their scales (one lane).
   __device__ __forceinline__ void load_w(const FewPos &q, int st) const {
@@ -419,18 +439,36 @@ struct FewKernel {
       if (!C::DOWN) bulk_load(dst + C::o_sc + C::sc_mat, p.ws[1] + at, n, bar);
     }
   }
-  // Token rows (all lanes).
+  // Token rows, and their block scales.  A bulk copy is issued lane by lane, so long rows (512
+  // bytes and more of a stage) go as one copy each, short ones as 16 bytes per lane.  Columns past K
+  // are not loaded and not used.
   __device__ __forceinline__ void load_x(const FewPos &q, int st, int lane) const {
-    const uint32_t dst = ring + st * C::stage, bar = smem_u32(&full[st]);
-    const int nr = min(q.cnt, 8 * C::NT);
-    const uint32_t w = width(q);
-    for (int n = lane; n < nr; n += 32) {
-      const uint32_t v = l.ent[q.n0 + n];
-      const size_t row = C::DOWN ? v & 0xFFFFu : v >> 16;
-      const size_t at = row * K + q.chunk * C::CH;
-      bulk_load(dst + C::o_x + n * C::x_row, p.xin + at, w * 2, bar);
-      if (C::BR == 2) bulk_load(dst + C::o_x + (8 * C::NT + n) * C::x_row, p.xlo + at, w * 2, bar);
-      if (C::SB) bulk_load(dst + C::o_sb + n * C::sb_row, p.xscale + (at >> 5), w >> 3, bar);
+    const uint32_t dst = ring + st * C::stage;
+    const int nr = min(q.cnt, 8 * C::NT), w = width(q);
+    const size_t k0 = (size_t)q.chunk * C::CH;
+    if constexpr (C::xbulk) {
+      const uint32_t bar = smem_u32(&full[st]);
+      for (int n = lane; n < nr; n += 32) {
+        const uint32_t v = l.ent[q.n0 + n], d = dst + C::o_x + n * C::x_row;
+        const size_t at = (size_t)(C::DOWN ? v & 0xFFFFu : v >> 16) * K + k0;
+        bulk_load(d, p.xin + at, w * 2, bar);
+        if (C::BR == 2) bulk_load(d + 8 * C::NT * C::x_row, p.xlo + at, w * 2, bar);
+        if (C::SB) bulk_load(dst + C::o_sb + n * C::sb_row, p.xscale + (at >> 5), w >> 3, bar);
+      }
+    } else {
+      static_assert(C::xbulk || !C::SB, "block scales come with long rows");
+      constexpr int segs = C::CH / 8;
+#pragma unroll 4
+      for (int i = lane; i < nr * segs; i += 32) {
+        const int n = i / segs, seg = i % segs;
+        if (seg * 8 >= w) continue;
+        const uint32_t v = l.ent[q.n0 + n];
+        const size_t at = (size_t)(C::DOWN ? v & 0xFFFFu : v >> 16) * K + k0 + seg * 8;
+        const uint32_t d = dst + C::o_x + n * C::x_row + seg * 16;
+        cp16(d, p.xin + at);
+        if (C::BR == 2) cp16(d + 8 * C::NT * C::x_row, p.xlo + at);
+      }
+      cp_arrive(&full[st]);
     }
   }
 
@@ -460,7 +498,7 @@ struct FewKernel {
         mbar_arrive_expect_tx(&full[st], bytes(q));
         load_w(q, st);
       }
-      __syncwarp();  // the expected bytes are set before any of them can arrive
+      if (C::xbulk) __syncwarp();  // the expected bytes are set before any of them can arrive
       load_x(q, st, lane);
       ++issued;
       next(q);
@@ -477,7 +515,7 @@ struct FewKernel {
   // ---- the multiplying warps ----
 
   // Four blocks (128 columns, a slice) of a warp's 16 rows times the token tiles, added to acc
-  // times two (done() halves the sums): 2^(s - 126) has the exponent field s + 1, which is
+  // times two (the entries' factors halve them): 2^(s - 126) has the exponent field s + 1, which is
   // right for every s up to 253, 0 included.  LARGE: for scale bytes above 127 in the stage (254
   // and 255, NaN, among them), the factor 2^(s - 127) made case by case.  wl: this lane's word of
   // row lane / 4 in the slice; xb, sb: its token row and the token scales.
@@ -697,7 +735,7 @@ __device__ __forceinline__ uint8_t *few_setup(uint8_t *raw, uint64_t *&full, uin
   abort_flag = reinterpret_cast<volatile int *>(smem + C::o_bars + 120);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::P; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], C::xbulk ? 1 : 1 + 32);  // bulk bytes, and the lanes' own copies
       mbar_init(&empty[i], C::warps);
     }
     *abort_flag = 0;
@@ -717,7 +755,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
   pdl_wait();
   pdl_trigger();
-  const int na = few_lists<C::threads>(p, l, &s_act);
+  const int na = few_lists<C>(p, l, &s_act);
   const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.h,
                        (p.h + C::CH - 1) / C::CH, na, p.f / C::outs, (int)gridDim.x, 0, 0};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -736,7 +774,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
           if (n >= q.cnt) continue;
           const uint32_t en = l.ent[q.n0 + n];
           if constexpr (C::MX4) {
-            const float xs = 0.5f * __ldg(p.xscale + (en >> 16));
+            const float xs = l.fac[q.n0 + n];
             hb[n * C::hrow + col] = silu_f(v[c] * xs) * (v[2 + c] * xs);
           } else {
             const float hv = silu_f(v[c]) * v[2 + c];
@@ -783,7 +821,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p.E, p.T * p.k));
   // Before the wait for k_few_glu: only what was complete when that kernel passed its own
   // wait (it lets this one start after that): the routing, and the caller's W2.
-  const int na = few_lists<C::threads>(p, l, &s_act);
+  const int na = few_lists<C>(p, l, &s_act);
   const int G = p.groups, rank = (int)cluster_ctarank();
   const int chunks = (p.f + C::CH - 1) / C::CH;
   const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.f, chunks, na,
@@ -805,7 +843,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
             const int n = 8 * nt + t2 + c;
             if (n >= q.cnt) continue;
             const uint32_t en = l.ent[q.n0 + n];  // an expert's entries: distinct tokens
-            const float w = few_weight(p, en & 0xFFFFu, q.e) * (C::MX4 ? 0.5f : 1.0f);
+            const float w = l.fac[q.n0 + n];
             float *y = ysum + (en >> 16) * C::yrow + r * 16 + g;
             y[0] = fmaf(w, v[c], y[0]);
             y[8] = fmaf(w, v[2 + c], y[8]);
@@ -934,18 +972,53 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
 
 // 4-bit weights whose rows are whole 128-byte pieces (K a multiple of 256) are fetched in boxes of
 // 128-byte rows, others in boxes of 64-byte rows.
-template <bool MX4, int NT, int R, int S, int KU, int PG, int CG, int PD, int CD>
+template <class G, class D>
 cudaError_t launch_few_pair(const FewParams &p, const FewParams &d, cudaStream_t st) {
-  cudaError_t e = MX4 && p.h % 256 == 0
-                      ? launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG, CG, MX4>>(p, st)
-                      : launch_few_glu<FewCfg<MX4, false, NT, R, S, KU, PG, CG>>(p, st);
-  if (e != cudaSuccess) return e;
-  return MX4 && p.f % 256 == 0
-             ? launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD, CD, MX4>>(d, st)
-             : launch_few_down<FewCfg<MX4, true, NT, R, S, KU, PD, CD>>(d, st);
+  const cudaError_t e = launch_few_glu<G>(p, st);
+  return e == cudaSuccess ? launch_few_down<D>(d, st) : e;
+}
+
+// Shape of a product: R row tiles x S slices of KU columns, P stages, CTAs per SM.
+template <int R_, int S_, int KU_, int P_, int CTAS_>
+struct FewShape {
+  static constexpr int R = R_, S = S_, KU = KU_, P = P_, CTAS = CTAS_;
+};
+
+// 4-bit weights whose rows are whole 128-byte pieces (K a multiple of 256) are fetched in boxes of
+// 128-byte rows, others in boxes of 64-byte rows.
+template <bool MX4, int NT, class G, class D>
+cudaError_t launch_few_shapes(const FewParams &p, const FewParams &d, cudaStream_t st) {
+  using G0 = FewCfg<MX4, false, NT, G::R, G::S, G::KU, G::P, G::CTAS>;
+  using D0 = FewCfg<MX4, true, NT, D::R, D::S, D::KU, D::P, D::CTAS>;
+  if constexpr (MX4) {
+    constexpr bool gw = G::KU % 256 == 0 || G::S % 2 == 0, dw = D::KU % 256 == 0 || D::S % 2 == 0;
+    using G1 = FewCfg<MX4, false, NT, G::R, G::S, G::KU, G::P, G::CTAS, true>;
+    using D1 = FewCfg<MX4, true, NT, D::R, D::S, D::KU, D::P, D::CTAS, true>;
+    static_assert(gw && dw && G::KU == 256 && D::KU == 256, "slices of 256 columns");
+    if (p.h % 256 == 0)
+      return p.f % 256 == 0 ? launch_few_pair<G1, D1>(p, d, st) : launch_few_pair<G1, D0>(p, d, st);
+    return p.f % 256 == 0 ? launch_few_pair<G0, D1>(p, d, st) : launch_few_pair<G0, D0>(p, d, st);
+  } else {
+    return launch_few_pair<G0, D0>(p, d, st);
+  }
 }
 
 }  // namespace
+
+using MG1 = FewShape<4, 2, 256, 3, 2>;
+using MD1 = FewShape<4, 2, 256, 3, 2>;
+using MG2 = FewShape<4, 2, 256, 2, 2>;
+using MD2 = FewShape<4, 2, 256, 2, 2>;
+using MG4 = FewShape<8, 1, 256, 2, 2>;
+using MD4 = FewShape<8, 1, 256, 2, 2>;
+using BG1 = FewShape<1, 8, 64, 4, 2>;
+using BD1 = FewShape<1, 8, 64, 3, 2>;
+using BG2 = FewShape<2, 4, 64, 4, 2>;
+using BD2 = FewShape<2, 4, 64, 3, 2>;
+using BG4 = FewShape<4, 2, 64, 4, 2>;
+using BD4 = FewShape<4, 2, 64, 3, 2>;
+using BG8 = FewShape<8, 1, 64, 4, 2>;
+using BD8 = FewShape<8, 1, 64, 3, 2>;
 
 cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renorm, int32_t *top,
                        float *weights, int32_t *status, cudaStream_t st) {
@@ -968,17 +1041,15 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   const double mean = (double)p.T * p.k / p.E;
   int nt = p.T <= 8 || mean <= 3 ? 1 : p.T <= 16 || mean <= 8 ? 2 : p.T <= 32 || mean <= 20 ? 4 : 8;
   if (var) nt = var;
-  const long long n = (long long)p.T * p.k, used = n < p.E ? n : p.E;
   if (mx4) {
-    if (var ? var == 16 : used * (p.f / 64) < device_sm_count() && nt == 1) return launch_few_pair<true, 1, 4, 2, 256, 3, 2, 3, 2>(p, d, st);
-    if (nt == 1) return launch_few_pair<true, 1, 8, 1, 256, 3, 3, 3, 3>(p, d, st);
-    if (nt == 2) return launch_few_pair<true, 2, 8, 1, 256, 3, 2, 3, 2>(p, d, st);
-    return launch_few_pair<true, 4, 8, 1, 256, 2, 2, 2, 2>(p, d, st);
+    if (nt == 1) return launch_few_shapes<true, 1, MG1, MD1>(p, d, st);
+    if (nt == 2) return launch_few_shapes<true, 2, MG2, MD2>(p, d, st);
+    return launch_few_shapes<true, 4, MG4, MD4>(p, d, st);
   }
-  if (nt == 1) return launch_few_pair<false, 1, 1, 8, 64, 4, 2, 3, 2>(p, d, st);
-  if (nt == 2) return launch_few_pair<false, 2, 2, 4, 64, 4, 2, 3, 2>(p, d, st);
-  if (nt == 4) return launch_few_pair<false, 4, 4, 2, 64, 3, 2, 3, 2>(p, d, st);
-  return launch_few_pair<false, 8, 8, 1, 64, 3, 2, 3, 2>(p, d, st);
+  if (nt == 1) return launch_few_shapes<false, 1, BG1, BD1>(p, d, st);
+  if (nt == 2) return launch_few_shapes<false, 2, BG2, BD2>(p, d, st);
+  if (nt == 4) return launch_few_shapes<false, 4, BG4, BD4>(p, d, st);
+  return launch_few_shapes<false, 8, BG8, BD8>(p, d, st);
 }
 
 }  // namespace dmoe
