@@ -21,8 +21,6 @@
 //     row (exact down to 2^-29 of the row's largest), H per 32 columns (11 bits); the 32
 //     products of a weight block are summed first, then scaled by the block's scale.
 // The few partial sums over S and over the experts of a token are added in a fixed order.
-#include <stdlib.h>
-
 #include <atomic>
 
 #include "common.cuh"
@@ -58,38 +56,71 @@ __device__ __forceinline__ uint32_t finite_abs(uint32_t b) {
 
 // One token's routing by one warp.  The k rounds of a warp-wide integer max over unique keys
 // (the logit's order-preserving image, then the lower expert) pick the top-k in rank order, as
-// the map's routing does; lane l holds experts l, l + 32, ...  The softmax terms use expf.
+// the map's routing does; lane l holds experts l, l + 32, ..., up to 256 experts in registers.
+// The softmax terms use expf.  Lane s < k returns pick s and its weight; `bad`: a logit is not
+// finite.
 __device__ __forceinline__ void route_token(const uint16_t *__restrict__ row, int E, int k,
-                                            bool renorm, int32_t *__restrict__ top,
-                                            float *__restrict__ weights, int32_t *status,
-                                            int lane) {
-  bool bad = false;
-  for (int e = lane; e < E; e += 32) bad |= (row[e] & 0x7F80u) == 0x7F80u;
+                                            bool renorm, int lane, int &expert, float &weight,
+                                            bool &bad) {
+  auto image = [&](int e) -> uint32_t { return (uint32_t)__ldcg(row + e) << 16; };
+  auto key_of = [&](uint32_t im, int e) { return route_key_nan(im, 0xFFFFu - (uint32_t)e); };
+  constexpr int R = 8;  // experts per lane in registers
+  uint32_t im[R], key[R];
+  bad = false;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = lane + 32 * i;
+    im[i] = (e < E) ? image(e) : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = (e < E) ? key_of(im[i], e) : 0u;
+    bad |= (im[i] & 0x7F800000u) == 0x7F800000u;
+  }
+  for (int e = lane + 32 * R; e < E; e += 32) bad |= (image(e) & 0x7F800000u) == 0x7F800000u;
   uint32_t last = 0xFFFFFFFFu, mine = 0u;
   for (int s = 0; s < k; ++s) {  // the largest key below the last pick
     uint32_t best = 0u;
-    for (int e = lane; e < E; e += 32) {
-      const uint32_t key = route_key_nan((uint32_t)row[e] << 16, 0xFFFFu - (uint32_t)e);
-      if (key < last) best = max(best, key);
+#pragma unroll
+    for (int i = 0; i < R; ++i) best = max(best, key[i] < last ? key[i] : 0u);
+    for (int e = lane + 32 * R; e < E; e += 32) {
+      const uint32_t ke = key_of(image(e), e);
+      if (ke < last) best = max(best, ke);
     }
     last = __reduce_max_sync(0xFFFFFFFFu, best);
     if (lane == s) mine = last;
   }
-  const int e = 0xFFFF - (int)(mine & 0xFFFFu);
-  const float v = (lane < k) ? __uint_as_float((uint32_t)row[e] << 16) : 0.0f;
+  expert = (lane < k) ? 0xFFFF - (int)(mine & 0xFFFFu) : 0;
+  const float v = (lane < k) ? __uint_as_float(image(expert)) : 0.0f;
   const float m = __shfl_sync(0xFFFFFFFFu, v, 0);
   float sum = 0.0f;
   if (renorm) {
     if (lane < k) sum = expf(v - m);
   } else {
-    for (int i = lane; i < E; i += 32) sum += expf(__uint_as_float((uint32_t)row[i] << 16) - m);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (lane + 32 * i < E) sum += expf(__uint_as_float(im[i]) - m);
+    for (int e = lane + 32 * R; e < E; e += 32) sum += expf(__uint_as_float(image(e)) - m);
   }
   sum = warp_sum(sum);
+  weight = expf(v - m) / sum;
+  bad = __any_sync(0xFFFFFFFFu, bad);
+}
+
+// ... with its results stored; `status` may be NULL.
+__device__ __forceinline__ void route_store(const uint16_t *__restrict__ row, int E, int k,
+                                            bool renorm, int32_t *top, float *weights,
+                                            int32_t *status, int lane) {
+  int e;
+  float w;
+  bool bad;
+  route_token(row, E, k, renorm, lane, e, w, bad);
   if (lane < k) {
     top[lane] = e;
-    weights[lane] = expf(v - m) / sum;
+    weights[lane] = w;
   }
-  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(status, DMOE_STATUS_NONFINITE_LOGITS);
+  if (bad && lane == 0 && status) set_status(status, DMOE_STATUS_NONFINITE_LOGITS);
 }
 
 // Given experts: report ids outside [0, E) (their entries add nothing) and repeats.
@@ -140,7 +171,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   }
   if (warp == 0) {
     if (logits)
-      route_token(logits + t * E, E, k, renorm != 0, top + t * k, weights + t * k, status, lane);
+      route_store(logits + t * E, E, k, renorm != 0, top + t * k, weights + t * k, status, lane);
     else
       check_token(top + t * k, E, k, status, lane);
   } else if (x16) {
@@ -235,9 +266,10 @@ template <bool MX4_, bool DOWN_, int NT_, int R_, int S_, int KU_, int P_, int C
 struct FewCfg {
   static constexpr bool MX4 = MX4_, DOWN = DOWN_, SB = MX4 && DOWN, WIDE = WIDE_;
   static constexpr int NT = NT_, R = R_, S = S_, KU = KU_, P = P_;
-  static constexpr int warps = R * S, threads = 32 * warps + 32;
   static constexpr int min_ctas = CTAS_;  // CTAs per SM
   static constexpr int CH = S * KU;  // columns per stage
+  static constexpr bool xbulk = CH * 2 >= 512 && NT <= 2;  // see load_x()
+  static constexpr int warps = R * S, loaders = xbulk ? 1 : 4, threads = 32 * (warps + loaders);
   static constexpr int BR = (DOWN && !MX4) ? 2 : 1;
   // weights: [W1, W3 | W2][slices of SC columns][rows][row_b bytes], as TMA boxes land
   static constexpr int SC = MX4 ? (WIDE ? 256 : 128) : 64, slices = CH / SC;
@@ -249,7 +281,6 @@ struct FewCfg {
   // a multiple of 128 keeps the reads free of bank conflicts
   static constexpr int x_row = CH * 2 + (MX4 ? 64 : 16);
   static constexpr int x_bytes = BR * 8 * NT * x_row;
-  static constexpr bool xbulk = CH * 2 >= 512;
   static constexpr int sb_row = CH / 8 + 16;  // a token's block scales
   static constexpr int sb_bytes = SB ? 8 * NT * sb_row : 0;
   static constexpr int o_sc = w_bytes, o_x = o_sc + mats * sc_mat, o_sb = o_x + x_bytes;
@@ -270,26 +301,37 @@ struct FewCfg {
 
 // Bytes of the expert lists: entries [n] (j | token << 16), a factor of each [n] (DOWN: its
 // weight; GLU with 4-bit weights: the scale of its token's x), starts [E + 1], experts in use
-// (uint16).
-__host__ __device__ inline size_t few_list_bytes(int E, int n) {
-  const size_t a = (size_t)n * 8 + (size_t)(E + 1) * 4 + (size_t)(E < n ? E : n) * 2;
+// (uint16); and with the routing done in the kernel the experts and weights [n].
+__host__ __device__ inline size_t few_list_bytes(const FewParams &p) {
+  const int n = p.T * p.k;
+  const size_t a = (size_t)n * (p.logits ? 16 : 8) + (size_t)(p.E + 1) * 4 +
+                   (size_t)(p.E < n ? p.E : n) * 2;
   return (a + 15) / 16 * 16;
 }
 
 struct FewLists {
   uint32_t *ent;
   float *fac;
+  int32_t *top;    // the routing, if this kernel does it
+  float *weights;
   int *start;
   uint16_t *act;
-  __device__ __forceinline__ FewLists(uint8_t *base, int E, int n)
-      : ent(reinterpret_cast<uint32_t *>(base)), fac(reinterpret_cast<float *>(ent + n)),
-        start(reinterpret_cast<int *>(fac + n)), act(reinterpret_cast<uint16_t *>(start + E + 1)) {}
+  __device__ __forceinline__ FewLists(uint8_t *base, const FewParams &p) {
+    const int n = p.T * p.k, routed = p.logits ? n : 0;
+    ent = reinterpret_cast<uint32_t *>(base);
+    fac = reinterpret_cast<float *>(ent + n);
+    top = reinterpret_cast<int32_t *>(fac + n);
+    weights = reinterpret_cast<float *>(top + routed);
+    start = reinterpret_cast<int *>(weights + routed);
+    act = reinterpret_cast<uint16_t *>(start + p.E + 1);
+  }
 };
 
 // Expert of entry j, or -1 for one that is not listed: an id outside [0, E), or an expert that an
 // earlier slot of the token names too (its weights are added up, see few_weight).  Read through
 // L2: k_few_down comes here before it waits for the kernel in front of it.
-__device__ __forceinline__ int few_entry(const FewParams &p, int j) {
+__device__ __forceinline__ int few_entry(const FewParams &p, const FewLists &l, int j) {
+  if (p.logits) return l.top[j];  // routed here
   const int e = __ldcg(p.top + j);
   if (e < 0 || e >= p.E) return -1;
   if (p.given)  // computed experts are distinct
@@ -299,7 +341,8 @@ __device__ __forceinline__ int few_entry(const FewParams &p, int j) {
 }
 
 // Weight of expert e for the token of its listed entry j.
-__device__ __forceinline__ float few_weight(const FewParams &p, int j, int e) {
+__device__ __forceinline__ float few_weight(const FewParams &p, const FewLists &l, int j, int e) {
+  if (p.logits) return l.weights[j];
   float w = __ldcg(p.weights + j);
   if (p.given)
     for (int i = j + 1; i < j - j % p.k + p.k; ++i)
@@ -315,10 +358,28 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
   constexpr int THREADS = C::threads;
   const int n = p.T * p.k, lane = threadIdx.x & 31;
   int *start = l.start;
+  if (p.logits) {  // a few tokens: every CTA routes them, a warp each, the first one writes it down
+    for (int t = threadIdx.x >> 5; t < p.T; t += THREADS / 32) {
+      int e;
+      float w;
+      bool bad;
+      route_token(p.logits + (size_t)t * p.E, p.E, p.k, p.renorm, lane, e, w, bad);
+      if (lane < p.k) {
+        l.top[t * p.k + lane] = e;
+        l.weights[t * p.k + lane] = w;
+        if (!C::DOWN && blockIdx.x == 0) {
+          p.top_out[t * p.k + lane] = e;
+          p.weights_out[t * p.k + lane] = w;
+        }
+      }
+      if (!C::DOWN && blockIdx.x == 0 && bad && lane == 0)
+        set_status(p.status, DMOE_STATUS_NONFINITE_LOGITS);
+    }
+  }
   for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = 0;
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
-    const int e = few_entry(p, j);
+    const int e = few_entry(p, l, j);
     if (e >= 0) atomicAdd(&start[e], 1);
   }
   __syncthreads();
@@ -346,13 +407,13 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
   }
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
-    const int e = few_entry(p, j);
+    const int e = few_entry(p, l, j);
     if (e < 0) continue;
     const int at = atomicSub(&start[e], 1) - 1, t = j / p.k;
     l.ent[at] = (uint32_t)j | ((uint32_t)t << 16);
     // 4-bit products come out halved (see blocks())
     if (C::DOWN)
-      l.fac[at] = few_weight(p, j, e) * (C::MX4 ? 0.5f : 1.0f);
+      l.fac[at] = few_weight(p, l, j, e) * (C::MX4 ? 0.5f : 1.0f);
     else if (C::MX4)
       l.fac[at] = 0.5f * __ldcg(p.xscale + t);
   }
@@ -415,7 +476,7 @@ struct FewKernel {
   }
   __device__ __forceinline__ int tile_of(const FewPos &q) const { return C::DOWN ? tile : q.b; }
 
-  // ---- the loading warp ----
+  // ---- the loading warps (the first one brings the weights) ----
 
   // Columns of K in the stage, and the bytes that its copies bring.
   __device__ __forceinline__ int width(const FewPos &q) const {
@@ -439,10 +500,11 @@ struct FewKernel {
       if (!C::DOWN) bulk_load(dst + C::o_sc + C::sc_mat, p.ws[1] + at, n, bar);
     }
   }
-  // Token rows, and their block scales.  A bulk copy is issued lane by lane, so long rows (512
-  // bytes and more of a stage) go as one copy each, short ones as 16 bytes per lane.  Columns past K
-  // are not loaded and not used.
-  __device__ __forceinline__ void load_x(const FewPos &q, int st, int lane) const {
+  // Token rows, and their block scales.  A bulk copy is issued lane by lane, so few long rows (512
+  // bytes and more of a stage) go as one copy each, more or shorter ones as 16 bytes per lane of four
+  // loading warps (of one warp: 95 us instead of 70 for the first product of 96 tokens on a skewed
+  // router).  Columns past K are not loaded and not used.
+  __device__ __forceinline__ void load_x(const FewPos &q, int st, int loader, int lane) const {
     const uint32_t dst = ring + st * C::stage;
     const int nr = min(q.cnt, 8 * C::NT), w = width(q);
     const size_t k0 = (size_t)q.chunk * C::CH;
@@ -456,10 +518,9 @@ struct FewKernel {
         if (C::SB) bulk_load(dst + C::o_sb + n * C::sb_row, p.xscale + (at >> 5), w >> 3, bar);
       }
     } else {
-      static_assert(C::xbulk || !C::SB, "block scales come with long rows");
       constexpr int segs = C::CH / 8;
 #pragma unroll 4
-      for (int i = lane; i < nr * segs; i += 32) {
+      for (int i = 32 * loader + lane; i < nr * segs; i += 32 * C::loaders) {
         const int n = i / segs, seg = i % segs;
         if (seg * 8 >= w) continue;
         const uint32_t v = l.ent[q.n0 + n];
@@ -468,16 +529,26 @@ struct FewKernel {
         cp16(d, p.xin + at);
         if (C::BR == 2) cp16(d + 8 * C::NT * C::x_row, p.xlo + at);
       }
+      if constexpr (C::SB) {
+        constexpr int sbs = C::CH / 128;  // four blocks each
+        for (int i = 32 * loader + lane; i < nr * sbs; i += 32 * C::loaders) {
+          const int n = i / sbs, seg = i % sbs;
+          if (seg * 128 >= w) continue;
+          const size_t row = l.ent[q.n0 + n] & 0xFFFFu;
+          cp16(dst + C::o_sb + n * C::sb_row + seg * 16,
+               p.xscale + row * (K >> 5) + (k0 >> 5) + seg * 4);
+        }
+      }
       cp_arrive(&full[st]);
     }
   }
 
   // pre: the weights of the first stages are loaded before the wait for the earlier kernels.
-  __device__ __forceinline__ void produce(int item0, bool pre, int lane) const {
+  __device__ __forceinline__ void produce(int item0, bool pre, int loader, int lane) const {
     FewPos q = first(item0), w = q;
     if (pre) {
       for (int st = 0; st < C::P && w.on; ++st) {
-        if (lane == 0) {
+        if (loader == 0 && lane == 0) {
           mbar_arrive_expect_tx(&full[st], bytes(w));
           load_w(w, st);
         }
@@ -494,12 +565,12 @@ struct FewKernel {
         if (lane == 0) good = mbar_wait(&empty[st], phase ^ 1u, p.status, abort_flag) ? 1 : 0;
         if (!__shfl_sync(0xFFFFFFFFu, good, 0)) break;
       }
-      if (lane == 0 && !(pre && issued < C::P)) {
+      if (loader == 0 && lane == 0 && !(pre && issued < C::P)) {
         mbar_arrive_expect_tx(&full[st], bytes(q));
         load_w(q, st);
       }
       if (C::xbulk) __syncwarp();  // the expected bytes are set before any of them can arrive
-      load_x(q, st, lane);
+      load_x(q, st, loader, lane);
       ++issued;
       next(q);
       if (++st == C::P) {
@@ -735,7 +806,7 @@ __device__ __forceinline__ uint8_t *few_setup(uint8_t *raw, uint64_t *&full, uin
   abort_flag = reinterpret_cast<volatile int *>(smem + C::o_bars + 120);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::P; ++i) {
-      mbar_init(&full[i], C::xbulk ? 1 : 1 + 32);  // bulk bytes, and the lanes' own copies
+      mbar_init(&full[i], C::xbulk ? 1 : 1 + 32 * C::loaders);  // bulk bytes, and the lanes' own copies
       mbar_init(&empty[i], C::warps);
     }
     *abort_flag = 0;
@@ -752,15 +823,15 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   uint64_t *full, *empty;
   volatile int *abort_flag;
   uint8_t *smem = few_setup<C>(raw, full, empty, abort_flag);
-  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
+  const FewLists l(smem + C::o_lists, p);
   pdl_wait();
   pdl_trigger();
   const int na = few_lists<C>(p, l, &s_act);
   const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.h,
                        (p.h + C::CH - 1) / C::CH, na, p.f / C::outs, (int)gridDim.x, 0, 0};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == C::warps) {
-    k.produce(blockIdx.x, false, lane);
+  if (warp >= C::warps) {
+    k.produce(blockIdx.x, false, warp - C::warps, lane);
     return;
   }
   float *hb = reinterpret_cast<float *>(smem + C::o_hbuf);
@@ -817,8 +888,8 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   uint64_t *full, *empty;
   volatile int *abort_flag;
   uint8_t *smem = few_setup<C>(raw, full, empty, abort_flag);
-  const FewLists l(smem + C::o_lists, p.E, p.T * p.k);
-  float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p.E, p.T * p.k));
+  const FewLists l(smem + C::o_lists, p);
+  float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p));
   // Before the wait for k_few_glu: only what was complete when that kernel passed its own
   // wait (it lets this one start after that): the routing, and the caller's W2.
   const int na = few_lists<C>(p, l, &s_act);
@@ -829,8 +900,8 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   for (int i = threadIdx.x; i < p.T * C::yrow; i += C::threads) ysum[i] = 0.0f;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == C::warps) {
-    k.produce(rank, true, lane);
+  if (warp >= C::warps) {
+    k.produce(rank, true, warp - C::warps, lane);
   } else {
     pdl_wait();
     pdl_trigger();
@@ -922,7 +993,7 @@ cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   p.ws[0] = static_cast<const uint8_t *>(p.w1.scales);
   p.ws[1] = static_cast<const uint8_t *>(p.w3.scales);
-  const size_t smem = C::fixed + few_list_bytes(p.E, p.T * p.k);
+  const size_t smem = C::fixed + few_list_bytes(p);
   const long long n = (long long)p.T * p.k;
   const long long items = (n < p.E ? n : p.E) * (p.f / C::outs);
   const long long ctas = few_places<C>(smem);
@@ -937,7 +1008,7 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   if (!few_map<C>(&p.tw[0], p.w2.data, (long long)p.E * p.h, p.f)) return cudaErrorInvalidValue;
   p.tw[1] = p.tw[0];
   p.ws[0] = p.ws[1] = static_cast<const uint8_t *>(p.w2.scales);
-  const size_t smem = C::fixed + few_list_bytes(p.E, p.T * p.k) +
+  const size_t smem = C::fixed + few_list_bytes(p) +
                       (size_t)p.T * C::y_row_bytes;
   const long long n = (long long)p.T * p.k;
   const int experts = (int)(n < p.E ? n : p.E);
@@ -949,7 +1020,9 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   while (G < 8 && tiles * G * 2 <= places) G *= 2;
   const int chunks = (p.f + C::CH - 1) / C::CH;
   int parts = 1;
-  while (experts * parts < G && parts * 2 <= chunks) parts *= 2;
+  while (parts * 2 <= chunks &&
+         (experts * parts < G || (experts * parts < 4 * G && chunks >= 16 * parts)))
+    parts *= 2;  // a long K in parts of eight chunks and more evens out the CTAs of a tile, too
   const int part = (chunks + parts - 1) / parts;
   p.kparts = (chunks + part - 1) / part;  // no empty part
   while (G > 1 && experts * p.kparts < G) G /= 2;
@@ -1005,30 +1078,61 @@ cudaError_t launch_few_shapes(const FewParams &p, const FewParams &d, cudaStream
 
 }  // namespace
 
+// The shapes of the first (G) and second (D) product, by weights (M: 4 bits, B: bf16) and token
+// tiles of 8.
 using MG1 = FewShape<4, 2, 256, 3, 2>;
 using MD1 = FewShape<4, 2, 256, 3, 2>;
 using MG2 = FewShape<4, 2, 256, 2, 2>;
 using MD2 = FewShape<4, 2, 256, 2, 2>;
 using MG4 = FewShape<8, 1, 256, 2, 2>;
-using MD4 = FewShape<8, 1, 256, 2, 2>;
+using MD4 = FewShape<4, 2, 256, 2, 1>;
 using BG1 = FewShape<1, 8, 64, 4, 2>;
-using BD1 = FewShape<1, 8, 64, 3, 2>;
+using BD1 = FewShape<2, 4, 64, 4, 2>;
 using BG2 = FewShape<2, 4, 64, 4, 2>;
 using BD2 = FewShape<2, 4, 64, 3, 2>;
-using BG4 = FewShape<4, 2, 64, 4, 2>;
+using BG4 = FewShape<4, 2, 64, 3, 2>;
 using BD4 = FewShape<4, 2, 64, 3, 2>;
-using BG8 = FewShape<8, 1, 64, 4, 2>;
-using BD8 = FewShape<8, 1, 64, 3, 2>;
+using BG8 = FewShape<8, 2, 64, 3, 1>;
+using BD8 = FewShape<8, 1, 64, 3, 1>;
+
+// Token tiles that a call's experts are given at a time.  An expert with more tokens reads its
+// weights again (from L2); one with fewer still has the larger tile's stages, fewer CTAs per SM
+// and rows to load.  The host knows T and the mean number of tokens per expert, mean = T k / E, not
+// the routing.
+//   4 bits: one tile up to 16 tokens (16 tokens, E = 64, top-8: 61 us, 69 with two), two up to a
+//     mean of 16 (64 tokens: 118 us, 136 with one, 114 to 156 with four), then four (128 tokens,
+//     E = 8, top-2, hidden 4096, ffn 14336: 670 us, 810 with two)
+//   bf16: up to 32 tokens one (32, E = 64, top-8: 140 us, 174 with two), from a mean of 4 on two
+//     (24, E = 16, top-4: 132 us, 142 with one); beyond that four, which a skewed router needs (96
+//     tokens, skewed: 117 us, 200 with one; 128 over E = 256: 306 us, 487 with one); from a mean of
+//     16 on eight (128 over E = 8: 740 us, 960 with four)
+static int few_token_tiles(bool mx4, int T, int k, int E) {
+  const long long n = (long long)T * k;
+  if (T <= 8) return 1;
+  if (mx4) return T <= 16 ? 1 : n < 16LL * E ? 2 : 4;
+  if (n >= 16LL * E) return 8;
+  return T > 32 ? 4 : n <= 4LL * E ? 1 : 2;
+}
 
 cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renorm, int32_t *top,
                        float *weights, int32_t *status, cudaStream_t st) {
   FewParams p = p_in;
   p.status = status;
+  p.renorm = renorm;
   const bool mx4 = p.w1.scales != nullptr;
-  cudaError_t e = launch_pdl(k_few_route, p.T, mx4 ? 32 * kRouteWarps : 32, 0, st, logits, p.E, p.k,
-                             renorm ? 1 : 0, p.h, top, weights, status,
-                             static_cast<const uint4 *>(p.x), reinterpret_cast<uint4 *>(p.x16),
-                             p.x16scale);
+  cudaError_t e = cudaSuccess;
+  // Up to 8 tokens (one per warp) and bf16 weights the two product kernels route the tokens
+  // themselves, in every CTA, instead of waiting for a kernel that does: one launch less (one
+  // token, E = 128, top-8: 11 us a call, 16 with it).
+  if (logits && !mx4 && p.T <= 8) {
+    p.logits = logits;
+    p.top_out = top;
+    p.weights_out = weights;
+  } else {
+    e = launch_pdl(k_few_route, p.T, mx4 ? 32 * kRouteWarps : 32, 0, st, logits, p.E, p.k,
+                   renorm ? 1 : 0, p.h, top, weights, status, static_cast<const uint4 *>(p.x),
+                   reinterpret_cast<uint4 *>(p.x16), p.x16scale);
+  }
   if (e != cudaSuccess) return e;
   FewParams d = p;
   p.xin = mx4 ? p.x16 : static_cast<const uint16_t *>(p.x);
@@ -1036,11 +1140,7 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   d.xin = p.hout;
   d.xlo = p.hlo;
   d.xscale = p.hscale;
-  const char *v = getenv("FEWV");
-  const int var = v ? atoi(v) : 0;
-  const double mean = (double)p.T * p.k / p.E;
-  int nt = p.T <= 8 || mean <= 3 ? 1 : p.T <= 16 || mean <= 8 ? 2 : p.T <= 32 || mean <= 20 ? 4 : 8;
-  if (var) nt = var;
+  const int nt = few_token_tiles(mx4, p.T, p.k, p.E);
   if (mx4) {
     if (nt == 1) return launch_few_shapes<true, 1, MG1, MD1>(p, d, st);
     if (nt == 2) return launch_few_shapes<true, 2, MG2, MD2>(p, d, st);

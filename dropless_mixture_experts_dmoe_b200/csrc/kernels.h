@@ -184,6 +184,11 @@ struct FewParams {
   CUtensorMap tw[2];  // W1 and W3, or W2
   const uint8_t *ws[2];
   int32_t *status;
+  // set where the product kernels route the tokens themselves
+  const uint16_t *logits;
+  bool renorm;
+  int32_t *top_out;
+  float *weights_out;
 };
 // logits given: top and weights are written first; else they are inputs.
 cudaError_t launch_few(const FewParams &p, const uint16_t *logits, bool renorm, int32_t *top,
