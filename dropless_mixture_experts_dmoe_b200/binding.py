@@ -178,8 +178,10 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:  # the raw handle: a torch Stream object costs a microsecond or three more
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:  # the raw handle: a torch Stream object costs three microseconds more
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -377,6 +379,22 @@ def dmoe_sparse_map_noalloc(dims: dmoe_dims, logits, smap: SparseMap, stream=Non
 
 # ---- serving: the layer for a few tokens, and the microscaled 4-bit format ------------------------
 
+def _device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _arg(name: str, t, shape: tuple, dtype, device: int) -> int:
+    """Address of an argument of the serving calls: a contiguous tensor of this shape and type on
+    the current CUDA device (a raw device address is passed on as it is)."""
+    if isinstance(t, int):
+        return t
+    if (t.get_device() != device or t.dtype != dtype or t.shape != shape or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"the current CUDA device; got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
 class Mx4:
     """A matrix, or a stack of expert matrices, in the microscaled 4-bit format (see dmoe_mx4 in
     include/dmoe.h): ``codes`` [..., rows, cols / 2] and ``scales`` [..., ceil(rows/128), cols/128,
@@ -389,9 +407,19 @@ class Mx4:
         self.shape = (*codes.shape[:-1], 2 * codes.shape[-1])
         if codes.dim() < 2 or tuple(scales.shape) != self.scales_shape(*self.shape):
             raise ValueError(f"scales of codes {tuple(codes.shape)}: {tuple(scales.shape)}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
         self.codes, self.scales = codes, scales
+        self._device = codes.get_device()
         self._c = dmoe_mx4(codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.byref(self._c)
+
+    def arg(self, name: str, shape: tuple, device: int):
+        """This matrix as an argument: of this shape, on the current CUDA device."""
+        if self.shape != shape or self._device != device:
+            raise ValueError(f"{name} must have shape {shape} on the current CUDA device; got "
+                             f"{self.shape} on {self.codes.device}")
+        return self.ref
 
     @staticmethod
     def scales_shape(*shape) -> tuple:
@@ -418,15 +446,19 @@ def _rows_cols(shape):
 def dmoe_mx4_quantize(src, dst: Mx4, stream=None):
     """dst = src (bf16, the shape of dst) in the microscaled 4-bit format."""
     rows, cols = _rows_cols(dst.shape)
-    _check(load().dmoe_mx4_quantize(rows, cols, _ptr(src), dst.ref, _stream(stream)),
+    dev = _device()
+    _check(load().dmoe_mx4_quantize(rows, cols, _arg("src", src, dst.shape, torch.bfloat16, dev),
+                                    dst.arg("dst", dst.shape, dev), _stream(stream)),
            "dmoe_mx4_quantize")
 
 
 def dmoe_mx4_dequantize(src: Mx4, dst, stream=None):
     """dst (bf16) = the values of src."""
     rows, cols = _rows_cols(src.shape)
-    _check(load().dmoe_mx4_dequantize(rows, cols, src.ref, _ptr(dst), _stream(stream)),
-           "dmoe_mx4_dequantize")
+    dev = _device()
+    _check(load().dmoe_mx4_dequantize(rows, cols, src.arg("src", src.shape, dev),
+                                      _arg("dst", dst, src.shape, torch.bfloat16, dev),
+                                      _stream(stream)), "dmoe_mx4_dequantize")
 
 
 class FewBuffers:
@@ -447,22 +479,44 @@ class FewBuffers:
                       self.status.data_ptr(), self.ws.data_ptr(), n)
 
 
+def _few_args(dims, x, logits, bufs, y, dev):
+    d = bufs.dims
+    if d is not dims and (d.T, d.hidden, d.ffn, d.num_experts, d.top_k) != (
+            dims.T, dims.hidden, dims.ffn, dims.num_experts, dims.top_k):
+        raise ValueError(f"the buffers are those of {d}, not of {dims}")
+    row = (dims.T, dims.hidden)
+    return (_arg("x", x, row, torch.bfloat16, dev),
+            None if logits is None else _arg("logits", logits, (dims.T, dims.num_experts),
+                                             torch.bfloat16, dev),
+            _arg("y", y, row, torch.bfloat16, dev))
+
+
 def dmoe_forward_few(dims: dmoe_dims, x, logits, w1, w3, w2, bufs: FewBuffers, y, stream=None):
     """The whole layer for T <= FEW_MAX_TOKENS tokens, from the logits [T,E] to y [T,h].  logits
     None: bufs.top_experts and bufs.weights are taken as given."""
+    dev = _device()
+    xp, lp, yp = _few_args(dims, x, logits, bufs, y, dev)
+    E, h, f, bf = dims.num_experts, dims.hidden, dims.ffn, torch.bfloat16
     top, weights, status, ws, n = bufs._args
-    _check(load().dmoe_forward_few(ctypes.byref(dims), _ptr(x), _ptr(logits), _ptr(w1), _ptr(w3),
-                                   _ptr(w2), top, weights, _ptr(y), status, ws, n,
-                                   _stream(stream)), "dmoe_forward_few")
+    _check(load().dmoe_forward_few(ctypes.byref(dims), xp, lp, _arg("w1", w1, (E, f, h), bf, dev),
+                                   _arg("w3", w3, (E, f, h), bf, dev),
+                                   _arg("w2", w2, (E, h, f), bf, dev), top, weights, yp, status,
+                                   ws, n, _stream(stream)),
+           "dmoe_forward_few")
 
 
 def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, bufs: FewBuffers,
                          y, stream=None):
     """dmoe_forward_few over expert weights in the microscaled 4-bit format."""
+    dev = _device()
+    xp, lp, yp = _few_args(dims, x, logits, bufs, y, dev)
+    E, h, f = dims.num_experts, dims.hidden, dims.ffn
     top, weights, status, ws, n = bufs._args
-    _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), _ptr(x), _ptr(logits), w1.ref, w3.ref,
-                                       w2.ref, top, weights, _ptr(y), status, ws, n,
-                                       _stream(stream)), "dmoe_mx4_forward_few")
+    _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), xp, lp, w1.arg("w1", (E, f, h), dev),
+                                       w3.arg("w3", (E, f, h), dev),
+                                       w2.arg("w2", (E, h, f), dev), top, weights, yp, status,
+                                       ws, n, _stream(stream)),
+           "dmoe_mx4_forward_few")
 
 
 class Mx4Buffers:
@@ -489,8 +543,13 @@ class Mx4Buffers:
 def dmoe_mx4_forward(dims: dmoe_dims, x, w1: Mx4, w3: Mx4, w2: Mx4, smap: SparseMap, y, ws,
                      stream=None):
     """y [T,h] = the layer with every product in the microscaled 4-bit format (inference)."""
-    _check(load().dmoe_mx4_forward(ctypes.byref(dims), _ptr(x), w1.ref, w3.ref, w2.ref,
-                                   ctypes.byref(smap.c), _ptr(y), _ptr(ws),
+    E, h, f, row = dims.num_experts, dims.hidden, dims.ffn, (dims.T, dims.hidden)
+    dev = _device()
+    _check(load().dmoe_mx4_forward(ctypes.byref(dims), _arg("x", x, row, torch.bfloat16, dev),
+                                   w1.arg("w1", (E, f, h), dev), w3.arg("w3", (E, f, h), dev),
+                                   w2.arg("w2", (E, h, f), dev), ctypes.byref(smap.c),
+                                   _arg("y", y, row, torch.bfloat16, dev),
+                                   _arg("ws", ws, ws.shape, ws.dtype, dev),
                                    ws.numel() * ws.element_size(), _stream(stream)),
            "dmoe_mx4_forward")
 

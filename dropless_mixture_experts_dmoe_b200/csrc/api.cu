@@ -246,10 +246,17 @@ FewLayout few_layout(const dmoe_dims *d) {
   return l;
 }
 
+// Rows of the stacked weights are int32 box coordinates.
+inline bool weight_rows_fit(const dmoe_dims *d) {
+  const long long m = d->hidden > d->ffn ? d->hidden : d->ffn;
+  return d->num_experts * m <= 0x7FFFFFFFLL;
+}
+
 inline int check_few_dims(const dmoe_dims *d) {
   int rc = check_dims(d);
   if (rc) return rc;
-  return (d->T <= DMOE_FEW_MAX_TOKENS && !rounding(d)) ? DMOE_OK : DMOE_ERR_SHAPE;
+  if (d->T > DMOE_FEW_MAX_TOKENS || rounding(d)) return DMOE_ERR_SHAPE;
+  return weight_rows_fit(d) ? DMOE_OK : DMOE_ERR_TOO_LARGE;
 }
 
 inline int check_mx4(const dmoe_mx4 *m) {
@@ -770,6 +777,7 @@ int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1, c
                      void *stream) {
   int rc = check_dims(dims);
   if (rc) return rc;
+  if (!weight_rows_fit(dims)) return DMOE_ERR_TOO_LARGE;
   if ((rc = check_map(map, true, dims))) return rc;
   if (!x || !y || !ws) return DMOE_ERR_NULL;
   rc = check_mx4(w1, w3, w2);
@@ -817,7 +825,7 @@ const char *dmoe_error_string(int code) {
     case DMOE_ERR_DEVICE:
       return "current device is not sm_100 (B200)";
     case DMOE_ERR_TOO_LARGE:
-      return "T*top_k or the padded row bound exceeds 2^31-1";
+      return "T*top_k, the padded row bound or the rows of the weights exceed 2^31-1";
     default:
       return "unknown error";
   }

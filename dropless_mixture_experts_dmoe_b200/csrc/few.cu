@@ -21,8 +21,6 @@
 //     row (exact down to 2^-29 of the row's largest), H per 32 columns (11 bits); the 32
 //     products of a weight block are summed first, then scaled by the block's scale.
 // The few partial sums over S and over the experts of a token are added in a fixed order.
-#include <atomic>
-
 #include "common.cuh"
 #include "kernels.h"
 #include "mx4.cuh"
@@ -33,7 +31,7 @@ namespace dmoe {
 namespace {
 
 constexpr int kRouteWarps = 8;
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kFewSmem = 226 * 1024;  // dynamic shared memory of a CTA at most
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -291,7 +289,7 @@ struct FewCfg {
   static constexpr int hrow = outs + 4;
   static constexpr int hbuf = (MX4 && !DOWN) ? 8 * NT * hrow * 4 : 0;
   // y sums: rows of `outs` plus 8 floats (four tokens x eight rows meet no bank twice)
-  static constexpr int yrow = DOWN ? outs + 8 : 0, y_row_bytes = yrow * 4;
+  enum { yrow = DOWN ? outs + 8 : 0 };
   static constexpr int o_red = P * stage, o_hbuf = o_red + red, o_bars = o_hbuf + hbuf,
                        o_lists = o_bars + 128;
   static constexpr int fixed = 1024 + o_lists;  // the ring starts on a 1024-byte boundary
@@ -946,19 +944,6 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
 
 // ---- host side ---------------------------------------------------------------------------------
 
-// Opt the kernel in to large shared memory, once per device.
-template <class Kernel>
-cudaError_t allow_smem(Kernel kernel, std::atomic<uint64_t> &done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = (dev < 64) ? 1ull << dev : 0ull;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 // Weights [rows, K] as slices of SC columns: {SC, rows, K / SC}; a box is a tile's rows of all the
 // slices of a stage (slices past K read zeros).
 template <class C>
@@ -986,7 +971,7 @@ int few_places(size_t smem) {
 template <class C>
 cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_few_glu<C>, done);
+  cudaError_t e = allow_smem(k_few_glu<C>, done, kFewSmem);
   if (e != cudaSuccess) return e;
   const long long ef = (long long)p.E * p.f;
   if (!few_map<C>(&p.tw[0], p.w1.data, ef, p.h) || !few_map<C>(&p.tw[1], p.w3.data, ef, p.h))
@@ -1003,13 +988,13 @@ cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
 template <class C>
 cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_few_down<C>, done);
+  cudaError_t e = allow_smem(k_few_down<C>, done, kFewSmem);
   if (e != cudaSuccess) return e;
   if (!few_map<C>(&p.tw[0], p.w2.data, (long long)p.E * p.h, p.f)) return cudaErrorInvalidValue;
   p.tw[1] = p.tw[0];
   p.ws[0] = p.ws[1] = static_cast<const uint8_t *>(p.w2.scales);
   const size_t smem = C::fixed + few_list_bytes(p) +
-                      (size_t)p.T * C::y_row_bytes;
+                      (size_t)p.T * C::yrow * sizeof(float);
   const long long n = (long long)p.T * p.k;
   const int experts = (int)(n < p.E ? n : p.E);
   const int tiles = p.h / C::outs;

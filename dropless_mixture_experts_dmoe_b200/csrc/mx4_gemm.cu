@@ -549,13 +549,12 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   const long long per_unit = 2LL * XM * p.k_tiles * 64;
   const long long group = (40LL << 20) / per_unit;
   p.group = (int)(group < 1 ? 1 : group > 64 ? 64 : group);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k_mx4_gemm<GLU>, done, (int)MxCfg<GLU>::smem);
+  if (e != cudaSuccess) return e;
   static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
   static int max_clusters = 0;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_mx4_gemm<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)MxCfg<GLU>::smem);
-    if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
     cfg.blockDim = dim3(X_THREADS, 1, 1);
@@ -565,7 +564,6 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
       n = device_sm_count() / 2;
     max_clusters = n;
   });
-  if (attr_err != cudaSuccess) return attr_err;
   const long long max_tiles = ((long long)g.nblk_cap / 2 + g.E) * p.n_tiles;
   // t * ceil(2^32 / n) / 2^32 truncates to t / n while t * n < 2^32
   p.n_magic = (p.n_tiles > 1 && max_tiles * p.n_tiles < (1LL << 32))

@@ -451,7 +451,9 @@ DMOE_API int dmoe_router_backward(const dmoe_dims *dims, const void *x, const vo
  *   ws: dmoe_workspace_bytes(dims, DMOE_WS_FEW) bytes.
  * Needs no map.  DMOE_ROUTE_RENORMALIZE is followed; DMOE_SAVE_X_ONLY and DMOE_FUSED_COMBINE
  * choose between forms of dmoe_forward and change nothing here; DMOE_ROUTE_TOKEN_ROUNDING and
- * T > DMOE_FEW_MAX_TOKENS are DMOE_ERR_SHAPE.  Results are deterministic. */
+ * T > DMOE_FEW_MAX_TOKENS are DMOE_ERR_SHAPE.  x and y may be the same rows.  Results are
+ * deterministic.  From about 16 tokens per expert on, dmoe_sparse_map + dmoe_forward (whole
+ * 128-row blocks on the tensor cores) take less time. */
 DMOE_API int dmoe_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
                               const void *w1, const void *w3, const void *w2,
                               int32_t *top_experts, float *weights, void *y, int32_t *status,
@@ -478,11 +480,12 @@ typedef struct {
  * s = floor(log2 m) - 2 + 127 kept within [0, 254] (0 for an all-zero block) and every element
  * the nearest e2m1 value to x / 2^(s - 127), ties to the even mantissa, saturated at +-6.  A
  * block that holds an inf or NaN gets the scale NaN and zero codes.  Scale bytes of the rows
- * that fill the last tile are written as 0. rows >= 1. */
+ * that fill the last tile are written as 0. rows >= 1.  DMOE_ERR_SHAPE for
+ * rows < 1 or cols not a multiple of 128, DMOE_ERR_TOO_LARGE past 2^40 rows or 2^30 columns. */
 DMOE_API int dmoe_mx4_quantize(int64_t rows, int64_t cols, const void *src, const dmoe_mx4 *dst,
                                void *stream);
 /* src -> dst [rows, cols] bf16: element times scale.  Exact, except that a product beyond bf16's
- * largest value (scale bytes 252 and above) is an inf. */
+ * largest value (scale bytes 253 and 254) is an inf. */
 DMOE_API int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src, void *dst,
                                  void *stream);
 

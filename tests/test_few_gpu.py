@@ -282,3 +282,77 @@ def test_few_decode_loop_follows_its_router(E, k):
         d["x"].copy_((d["x"].float() + y.float()).bfloat16())
         d["logits"].copy_(torch.roll(d["logits"], 1, 1))
     assert int(bufs.status.item()) == 0
+
+
+def test_few_extreme_weight_scales():
+    """4-bit weights with scale bytes 0 (2^-127), 1, above 127 and NaN: the right values, and NaN
+    only where a NaN scale meets a row."""
+    T, h, f, E, k = shape = (5, 512, 256, 4, 2)
+    d = make(shape, seed=21, mx4=True)
+    d["x"] *= 2.0 ** -10
+    d["w1"].scales[0, 0, 0] = 0       # rows 0..127, columns 0..127 of expert 0
+    d["w1"].scales[1, 1, 2, :, :, 3] = 1
+    d["w3"].scales[2, 0, 1, 5] = 133  # 2^6
+    d["w2"].scales[3, 1, 0, :, 1, 2] = 128
+    d["w2"].scales[1, 0, 0, 7, 2, 1] = 255  # row 32 * 2 + 7 of expert 1
+    for w in ("w1", "w3", "w2"):
+        d[w + "_64"] = R.mx4_decode_values(d[w].codes, d[w].scales)
+    top = torch.tensor([[0, 2], [1, 3], [2, 3], [3, 0], [0, 3]]).cuda()
+    bufs, yg = outputs(d)
+    bufs.top_experts.copy_(top)
+    bufs.weights.fill_(0.5)
+    run(d, bufs, yg[:-1], logits=None)
+    torch.cuda.synchronize()
+    y, tol = reference(d, top, bufs.weights.double())
+    nan = torch.isnan(y)
+    assert nan.sum() == 1 and bool(nan[1, 71])
+    assert torch.equal(torch.isnan(yg[:-1]), nan)
+    R.check(yg[:-1][~nan], y[~nan], tol[~nan], "y")
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_few_in_place_and_back_to_back(mx4):
+    """y over x, and calls of different shapes one after the other on one stream with no
+    synchronisation between them: the bits of isolated calls."""
+    shapes = [(1, 256, 128, 8, 2), (40, 512, 384, 16, 4), (9, 128, 256, 64, 8), (8, 384, 128, 4, 4)]
+    ds = [make(s, seed=i, mx4=mx4) for i, s in enumerate(shapes)]
+    ref = []
+    for d in ds:
+        bufs, yg = outputs(d)
+        run(d, bufs, yg[:-1])
+        torch.cuda.synchronize()
+        ref.append(yg[:-1].clone())
+    state = [outputs(d) for d in ds]
+    for _ in range(30):
+        for d, (bufs, yg) in zip(ds, state):
+            run(d, bufs, yg[:-1])
+    for (bufs, yg), r in zip(state, ref):
+        assert same(yg[:-1], r)
+    for d, (bufs, _), r in zip(ds, state, ref):
+        run(d, bufs, d["x"])
+        assert same(d["x"], r)
+
+
+def test_few_follows_weights_written_just_before():
+    """Each call comes right behind the kernels that wrote its weights, logits and x: nothing is
+    read before they are done."""
+    T, h, f, E, k = shape = (4, 1024, 512, 8, 2)
+    d = make(shape, seed=2)
+    w = {n: torch.stack([d[n], d[n].flip(1)]) for n in ("w1", "w3", "w2", "x", "logits")}
+    ref = []
+    for i in range(2):
+        for n in w:
+            d[n].copy_(w[n][i])
+        torch.cuda.synchronize()
+        bufs, yg = outputs(d)
+        run(d, bufs, yg[:-1])
+        torch.cuda.synchronize()
+        ref.append(yg[:-1].clone())
+    bufs, _ = outputs(d)
+    ys = [torch.empty_like(d["x"]) for _ in range(20)]
+    for i, y in enumerate(ys):
+        for n in w:
+            d[n].copy_(w[n][i % 2])
+        run(d, bufs, y)
+    for i, y in enumerate(ys):
+        assert same(y, ref[i % 2]), i

@@ -1,4 +1,6 @@
 """The microscaled 4-bit format and the layer that runs in it, against definitions in 64 bits."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -282,3 +284,39 @@ def test_mx4_prompt_then_decode():
     torch.cuda.synchronize()
     assert torch.equal(y.view(torch.int16), ref[0].view(torch.int16))
     assert torch.equal(y2.view(torch.int16), ref[1].view(torch.int16))
+
+
+def test_mx4_forward_given_experts_all_absent():
+    """Given experts, every id out of range: no block at all, y is zero, the map says so."""
+    dims, x, lg, w, bufs = setup((70, 256, 128, 4, 2, 0))
+    bufs.map.top_experts.fill_(-1)
+    bufs.map.weights.fill_(1.0)
+    y = torch.full_like(x, float("nan"))
+    B.dmoe_sparse_map(dims, None, bufs.map, bufs.ws_map)
+    B.dmoe_mx4_forward(dims, x, *w, bufs.map, y, bufs.ws)
+    torch.cuda.synchronize()
+    assert int(bufs.map.num_blocks.item()) == 0
+    assert int(bufs.map.status.item()) == B.STATUS_EXPERT_OUT_OF_RANGE
+    assert (y == 0).all()
+
+
+def test_mx4_forward_stall_reports_timeout_and_context_survives():
+    """A first stage that is withheld on purpose: the waits run out, the status says so, and the
+    next call is right again."""
+    dims, x, lg, w, bufs = setup((600, 256, 384, 8, 2, 0))
+    y, y2 = torch.empty_like(x), torch.empty_like(x)
+    B.dmoe_sparse_map(dims, lg, bufs.map, bufs.ws_map)
+    B.dmoe_mx4_forward(dims, x, *w, bufs.map, y, bufs.ws)
+    torch.cuda.synchronize()
+    assert int(bufs.map.status.item()) == 0
+    B.dmoe_debug_inject_stall(True)
+    t0 = time.time()
+    B.dmoe_mx4_forward(dims, x, *w, bufs.map, y2, bufs.ws)
+    torch.cuda.synchronize()
+    assert int(bufs.map.status.item()) & B.STATUS_TIMEOUT
+    assert time.time() - t0 < 10.0
+    B.dmoe_sparse_map(dims, lg, bufs.map, bufs.ws_map)
+    B.dmoe_mx4_forward(dims, x, *w, bufs.map, y2, bufs.ws)
+    torch.cuda.synchronize()
+    assert int(bufs.map.status.item()) == 0
+    assert torch.equal(y.view(torch.int16), y2.view(torch.int16))

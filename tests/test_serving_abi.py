@@ -120,3 +120,37 @@ def test_reference_of_the_format():
     assert e.tolist() == [[0.0, -2.0]]
     assert q[0, 0, :8].tolist() == [6, 4, 2, 4, -0.0, -1, 0.5, 6]
     assert q[0, 1, :4].tolist() == [4, 2, -0.0, 0.5]
+
+
+def test_binding_checks_tensors_on_the_host():
+    """Wrong device, type, shape or layout is a ValueError before the library is called."""
+    d = B.make_dims(4, 256, 128, 8, 2)
+    few = B.FewBuffers(d, device="cpu")
+    bf = dict(dtype=torch.bfloat16)
+    x, lg = torch.zeros(4, 256, **bf), torch.zeros(4, 8, **bf)
+    w1, w2 = torch.zeros(8, 128, 256, **bf), torch.zeros(8, 256, 128, **bf)
+    q1, q2 = B.Mx4.empty(8, 128, 256, device="cpu"), B.Mx4.empty(8, 256, 128, device="cpu")
+    with pytest.raises(ValueError, match="x must be"):
+        B.dmoe_forward_few(d, x, lg, w1, w1, w2, few, x)
+    with pytest.raises(ValueError, match="x must be"):
+        B.dmoe_forward_few(d, x.t(), lg, w1, w1, w2, few, x)
+    with pytest.raises(ValueError, match="w1 must be"):
+        B.dmoe_forward_few(d, FAKE, FAKE, w1, w1, w2, few, FAKE)
+    with pytest.raises(ValueError, match="w1 must have"):
+        B.dmoe_mx4_forward_few(d, FAKE, FAKE, q2, q1, q2, few, FAKE)
+    with pytest.raises(ValueError, match="buffers"):
+        B.dmoe_forward_few(B.make_dims(3, 256, 128, 8, 2), x, lg, w1, w1, w2, few, x)
+    with pytest.raises(ValueError, match="src must be"):
+        B.dmoe_mx4_quantize(w1, q1)
+    with pytest.raises(ValueError, match="src must have"):
+        B.dmoe_mx4_dequantize(q1, w1)
+
+
+def test_weights_too_tall(lib):
+    """Rows of the stacked weights past 31 bits."""
+    d = B.make_dims(4, 2 ** 22, 128, 1024, 2)
+    assert few(lib, d) == -8 and few(lib, d, True) == -8
+    m = B.dmoe_map(*([FAKE] * len(B.MAP_FIELDS)))
+    w = B.dmoe_mx4(FAKE, FAKE)
+    r = ctypes.byref
+    assert lib.dmoe_mx4_forward(r(d), FAKE, r(w), r(w), r(w), r(m), FAKE, FAKE, 1 << 60, None) == -8
