@@ -11,15 +11,17 @@
 // pair of consecutive row blocks of one expert times a column tile, enumerated from padded_bins
 // on the device.  GLU tiles are 256 columns wide (128 of gate, 128 of up).  DOWN tiles are 128
 // wide with two accumulators: its K (ffn) is short, so that the hand-over of the accumulator,
-// not the operands, bounds it.  Persistent clusters of two CTAs, 576 threads each:
-//   warp 0      TMA producer: per stage of 256 K this CTA's 128 rows of A (16 KB, 128-byte
-//               swizzle), its half of B, the scale tiles of its A rows and of all rows of B (each
-//               SM of the pair multiplies by all of them)
-//   warp 1      one thread of the leader: tcgen05.cp of a stage's scale tiles into tensor memory
-//               (512-byte tiles, each 32 lanes x 4 columns repeated for the four lane groups) and
-//               four MMAs of 64 K.  The copies of the next stage go ahead of the MMAs of the
-//               current one when its data is there: the tensor pipe takes both in order, and an
-//               MMA right behind its own scales waits for them
+// not the operands, bounds it.  Persistent clusters of two CTAs, 608 threads each:
+//   warp 0      TMA producer: per stage of 256 K this CTA's half of B with 128-byte swizzle, and
+//               the scale tiles of all rows of B (each SM of the pair multiplies by all of them);
+//               and its 128 rows of A (16 KB) with their scales: GLU for every stage (a ring of six;
+//               a stage's round trip is about 4000 clocks, its MMAs 512), DOWN (K up to 1024) once
+//               per unit, which leaves room for a ring of nine stages of B.  Each pair takes a
+//               contiguous share of the tiles, a unit's columns in a row
+//   warp 18     leader only: tcgen05.cp of a stage's scale tiles into tensor memory (512-byte
+//               tiles, each 32 lanes x 4 columns repeated for the four lane groups)
+//   warp 1      leader only: four MMAs of 64 K per stage.  One warp that did both took 1000
+//               clocks a stage, where the MMAs take 512
 //   warps 2..17 epilogue: a warp takes 32 rows and 64 accumulator columns
 // Tensor memory: 256 accumulator columns, and 32 columns of scales per stage, which are
 // rewritten only after the stage's MMAs are done.  Two GLU accumulators and scales do not fit in
@@ -45,28 +47,33 @@ constexpr int XK = 256;            // K per stage: one 128-byte swizzle row of e
 constexpr int X_A = XM * XK / 2;   // A's bytes per stage and CTA: 16 KB
 constexpr int X_SF = 2 * kMx4TileBytes;  // scales of 128 rows: two column tiles
 constexpr int X_EPI = 16;
-constexpr int X_THREADS = 64 + 32 * X_EPI;
+constexpr int X_THREADS = 96 + 32 * X_EPI;
 constexpr int X_BOX = 32 * 128;  // a result box: 32 rows x 128 B
 constexpr int X_TMEM = 512;
-constexpr int X_SF_COL = 256;  // scales of stage s: columns 256 + 32 s ..
 
 // DOWN stages its results in one box per epilogue warp, GLU stores from registers.
 template <bool GLU>
 struct MxCfg {
   static constexpr int N = GLU ? 256 : 128;  // columns per tile (accumulator)
   static constexpr int nacc = GLU ? 1 : 2;
-  static constexpr int sfb = N / 128;            // 128-row scale tiles of B
+  static constexpr int sfb = N / 128;             // 128-row scale tiles of B
   static constexpr int b_bytes = N / 2 * XK / 2;  // this CTA's half of B
-  static constexpr int ops = X_A + b_bytes, sf = (1 + sfb) * X_SF, stage = ops + sf;
-  static constexpr int stages = GLU ? 6 : 5;
+  static constexpr int b_stage = b_bytes + sfb * X_SF, a_stage = X_A + X_SF;
+  static constexpr int stages = GLU ? 6 : 9;  // ring of B
+  static constexpr int slots = GLU ? 6 : 4;   // stages of A
   static constexpr int out = GLU ? 0 : X_EPI * X_BOX;
   static constexpr int amax = GLU ? 0 : X_EPI * 32 * 4;
   static constexpr int tables = 2;  // per expert: units and row blocks before it
-  static constexpr size_t smem = 1024 + (size_t)stages * stage + out + amax + 256 +
-                                 sizeof(int) * tables * (DMOE_MAX_EXPERTS + 1);
+  // barriers: full, empty, sfull [stages], tfull, tempty, drain [2]; the tensor-memory address and
+  // the abort flag behind them
+  static constexpr int bar_bytes = ((3 * stages + 6) * 8 + 8 + 127) / 128 * 128;
+  static constexpr size_t smem = 1024 + (size_t)stages * b_stage + (size_t)slots * a_stage + out +
+                                 amax + bar_bytes + sizeof(int) * tables * (DMOE_MAX_EXPERTS + 1);
+  // tensor memory: accumulators | scales of A's slots | scales of B's stages
+  static constexpr int sfa_col = 256, sfb_col = sfa_col + 8 * slots;
   // arrivals that release an accumulator: the epilogue warps of both CTAs that read it
   static constexpr int epi_arrivals = 2 * X_EPI / nacc;
-  static_assert(X_SF_COL + 32 * stages <= X_TMEM, "tensor memory");
+  static_assert(nacc * N <= sfa_col && sfb_col + 8 * sfb * stages <= X_TMEM, "tensor memory");
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -78,8 +85,7 @@ struct MxParams {
   const float *row_weight;  // DOWN: [P_max] routing weight of each padded row
   int E, h, f;
   int n_tiles, k_tiles;  // column tiles per unit; 128-wide K tiles
-  uint32_t n_magic;      // ceil(2^32 / n_tiles), or 0
-  int nblk_cap, group;
+  int nblk_cap;
   int inject;
   long long wait_cycles;
   uint8_t *hq, *hs;  // GLU
@@ -87,8 +93,9 @@ struct MxParams {
   int32_t *status;
 };
 
+// A tile: column tile n of unit vu (of all experts' units in a row), this CTA's rows.
 struct MxTile {
-  int e, n, row0;
+  int vu, n, e, row0;
   bool dummy;
 };
 
@@ -97,34 +104,38 @@ struct MxTables {
   const int *ustart, *bstart;
 };
 
-// Tile t -> expert, column tile, this CTA's rows; units of an expert in chunks of p.group, the
-// unit varying fastest so that concurrent pairs share B.
-__device__ __forceinline__ MxTile mx_decode(const MxParams &p, int t, const MxTables &tb,
-                                            uint32_t rank) {
-  // the expert whose units hold vu = t / n_tiles, the last one with ustart[e] <= vu: the whole
-  // warp looks, first at every 32nd expert, then at the 32 from there on
+// The expert and rows of tl.vu.  The whole warp looks for the last expert with ustart[e] <= vu,
+// first at every 32nd, then at the 32 from there on.
+__device__ __forceinline__ void mx_unit(const MxParams &p, MxTile &tl, const MxTables &tb,
+                                        uint32_t rank) {
   const int lane = threadIdx.x & 31;
-  // the tile counts divide by a multiplication: the host checked that it is exact for every t
-  const int vu = p.n_magic ? (int)__umulhi((uint32_t)t, p.n_magic) : t / p.n_tiles;
   const int g = 32 * lane, e0 =
-      32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < p.E && tb.ustart[min(g, p.E)] <= vu)) - 1);
-  const int c = e0 + lane, lo =
-      e0 + __popc(__ballot_sync(0xFFFFFFFFu, c < p.E && tb.ustart[min(c, p.E)] <= vu)) - 1;
-  const int u0 = tb.ustart[lo], units = tb.ustart[lo + 1] - u0;
-  int c0 = 0, cs = max(units, 1);  // (no units at all: nothing of the result is used)
-  if (units > p.group) {
-    c0 = ((vu - u0) / p.group) * p.group;
-    cs = min(p.group, units - c0);
-  }
-  const int lt = t - (u0 + c0) * p.n_tiles;
-  MxTile tl;
-  tl.e = lo;
-  // lt < group * n_tiles: small enough for the nearest float quotient of lt + 1/2 to truncate right
-  tl.n = (lt < (1 << 20)) ? (int)__fdividef((float)lt + 0.5f, (float)cs) : lt / cs;
-  const int unit = c0 + (lt - tl.n * cs);
-  const int b = tb.bstart[lo] + 2 * unit + (int)rank;
-  tl.dummy = b >= tb.bstart[lo + 1];
+      32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < p.E && tb.ustart[min(g, p.E)] <= tl.vu)) - 1);
+  const int c = e0 + lane;
+  tl.e = e0 + __popc(__ballot_sync(0xFFFFFFFFu, c < p.E && tb.ustart[min(c, p.E)] <= tl.vu)) - 1;
+  const int b = tb.bstart[tl.e] + 2 * (tl.vu - tb.ustart[tl.e]) + (int)rank;
+  tl.dummy = b >= tb.bstart[tl.e + 1];
   tl.row0 = (tl.dummy ? p.nblk_cap : b) * XM;  // past the last row: loads read zeros
+}
+
+// `by` tiles on: the columns of a unit first, then the next unit.
+__device__ __forceinline__ void mx_step(const MxParams &p, MxTile &tl, int by, const MxTables &tb,
+                                        uint32_t rank) {
+  tl.n += by;
+  if (tl.n < p.n_tiles) return;
+  while (tl.n >= p.n_tiles) {
+    tl.n -= p.n_tiles;
+    ++tl.vu;
+  }
+  mx_unit(p, tl, tb, rank);
+}
+
+__device__ __forceinline__ MxTile mx_first(const MxParams &p, int t, const MxTables &tb,
+                                           uint32_t rank) {
+  MxTile tl;
+  tl.vu = t / p.n_tiles;
+  tl.n = t - tl.vu * p.n_tiles;
+  mx_unit(p, tl, tb, rank);
   return tl;
 }
 
@@ -177,10 +188,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ int mx_snake(int r, int cluster, int nclusters) {
-  return r * nclusters + ((r & 1) ? nclusters - 1 - cluster : cluster);
-}
-
 // silu(z) u with one reciprocal: e^-z overflowing to inf gives 1 / inf = 0, the limit.
 __device__ __forceinline__ float silu_mul(float z, float u) {
   float r;
@@ -219,17 +226,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base_u32 = smem_u32(smem_raw);
   uint8_t *tiles = smem_raw + ((1024u - (base_u32 & 1023u)) & 1023u);
-  // operands of all stages first (1024-byte aligned), then result boxes, scales, barriers
   using C = MxCfg<GLU>;
   constexpr int X_STAGES = C::stages;
-  uint8_t *outbuf = tiles + X_STAGES * C::ops;
-  uint8_t *scales = outbuf + MxCfg<GLU>::out;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(scales + X_STAGES * C::sf);
+  uint8_t *abuf = tiles, *bbuf = abuf + C::slots * X_A;  // elements: 1024-byte aligned
+  uint8_t *outbuf = bbuf + X_STAGES * C::b_bytes;
+  uint8_t *ascale = outbuf + C::out, *bscale = ascale + C::slots * X_SF;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(bscale + X_STAGES * C::sfb * X_SF);
   uint64_t *full = bars, *empty = bars + X_STAGES;
-  uint64_t *tfull = bars + 2 * X_STAGES, *tempty = tfull + 2, *drain = tfull + 4;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 5);
+  uint64_t *sfull = bars + 2 * X_STAGES;  // leader: the stage's scales are in tensor memory
+  uint64_t *tfull = bars + 3 * X_STAGES, *tempty = tfull + 2, *drain = tfull + 4;  // [2] each
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 6);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  float *amax = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bars) + 256);
+  float *amax = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bars) + C::bar_bytes);
   int *ustart = reinterpret_cast<int *>(amax + MxCfg<GLU>::amax / 4);
   int *bstart = ustart + p.E + 1;  // [E + 1] each
   const MxTables tables{ustart, bstart};
@@ -243,12 +251,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     for (int s = 0; s < X_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sfull[s], 1);
     }
     for (int a = 0; a < C::nacc; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], C::epi_arrivals);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&p.ta);
@@ -286,94 +296,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   cluster_sync_all();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // this cluster's tiles: a contiguous share of all
   const int total = ustart[p.E] * p.n_tiles;
+  const int t0 = (int)((long long)cluster * total / nclusters);
+  const int t1 = (int)((long long)(cluster + 1) * total / nclusters);
   const int k_stages = (p.k_tiles + 1) / 2;
+  // DOWN: A stays in its slots while the unit's columns pass, in `groups` sets of slots by turns.
+  // GLU, and a K too long for the slots: A passes through with B, stage by stage.
+  const bool resident = !GLU && k_stages <= C::slots;
+  const int groups = resident ? C::slots / k_stages : 1;
+  const int ring = resident || GLU ? C::stages : C::slots;
   const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
   const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
 
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
-    int stage = 0;
+    int stage = 0, group = 0;
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    int t = mx_snake(0, cluster, nclusters);
-    MxTile tl = mx_decode(p, max(0, min(t, total - 1)), tables, rank), nx = tl;
-    for (int r = 0; ok && t < total; tl = nx) {
-      // the next tile is looked up once this one's first stage is on its way
-      const int tn = mx_snake(++r, cluster, nclusters);
+    MxTile tl = mx_first(p, min(t0, max(total - 1, 0)), tables, rank);
+    for (int t = t0; ok && t < t1; ++t) {
+      const bool fresh = t == t0 || tl.n == 0 || !resident;  // A has to be loaded
+      if (t != t0 && tl.n == 0 && ++group == groups) group = 0;
       // B rows: this CTA's half; scale row tiles of all of B
       const int brow =
           GLU ? tl.e * p.f + tl.n * 128 : tl.e * p.h + tl.n * 128 + (int)rank * 64;
-      const int s0 = brow / 128 * p.k_tiles, sa0 = tl.row0 / 128 * p.k_tiles;
+      const int s0 = brow / 128 * p.k_tiles, sa0 = tl.row0 / 128 * p.k_tiles, row0 = tl.row0;
       for (int kb = 0; kb < k_stages; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag, p.wait_cycles)) {
+        ok = mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag, p.wait_cycles);
+        if (resident && fresh) {  // the slot's last use, groups * k_stages stages ago at the latest
+          const int last = (int)issued - groups * k_stages, turn = last / ring;
+          if (ok && last >= 0)
+            ok = mbar_wait(&empty[last - turn * ring], (uint32_t)turn & 1u, p.status, abort_flag,
+                           p.wait_cycles);
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
         const uint32_t bar = leader_full0 + (uint32_t)(stage * sizeof(uint64_t));
         // test-only stall (inject): the first stage is never armed, so the MMA's wait on it expires
         if (!(p.inject && leader && issued == 0) && elect_one()) {
-          uint8_t *sa = tiles + stage * C::ops;
-          uint8_t *sf = scales + stage * C::sf;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::stage);
-          tma_load_2d_pair(sa, &p.ta, bar, kb * (XK / 2), tl.row0);
-          tma_load_2d_pair(sa + X_A, &p.tb[rank], bar, kb * (XK / 2), brow);
+          if (leader)
+            mbar_arrive_expect_tx(&full[stage], 2 * (C::b_stage + (fresh ? C::a_stage : 0)));
+          uint8_t *sf = bscale + stage * C::sfb * X_SF;
           // scale tiles of K tiles 2 kb, 2 kb + 1 (one past an odd end is loaded, not used)
-          tma_load_2d_pair(sf, &p.tsa, bar, 0, sa0 + 2 * kb);
-          tma_load_2d_pair(sf + X_SF, &p.tsb[0], bar, 0, s0 + 2 * kb);
-          if (GLU) tma_load_2d_pair(sf + 2 * X_SF, &p.tsb[1], bar, 0, s0 + 2 * kb);
+          tma_load_2d_pair(bbuf + stage * C::b_bytes, &p.tb[rank], bar, kb * (XK / 2), brow);
+          tma_load_2d_pair(sf, &p.tsb[0], bar, 0, s0 + 2 * kb);
+          if (GLU) tma_load_2d_pair(sf + X_SF, &p.tsb[1], bar, 0, s0 + 2 * kb);
+          if (fresh) {
+            const int slot = resident ? group * k_stages + kb : stage;
+            tma_load_2d_pair(abuf + slot * X_A, &p.ta, bar, kb * (XK / 2), row0);
+            tma_load_2d_pair(ascale + slot * X_SF, &p.tsa, bar, 0, sa0 + 2 * kb);
+          }
         }
-        if (kb == 0 && tn < total) nx = mx_decode(p, tn, tables, rank);
+        if (kb == 0) mx_step(p, tl, 1, tables, rank);  // the next tile, while this one loads
         ++issued;
-        if (++stage == X_STAGES) {
+        if (++stage == ring) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      t = tn;
     }
     __syncwarp();
     if (leader && lane == 0)  // every issued copy (of both CTAs) has landed before exit
-      for (long long i = (issued > X_STAGES ? issued - X_STAGES : 0); i < issued; ++i)
-        mbar_wait_plain(&full[i % X_STAGES], (uint32_t)((i / X_STAGES) & 1), p.wait_cycles);
-  } else if (warp == 1 && leader) {
-    // ---------------- scales and MMAs (leader only) ----------------
-    int n = 0;  // stages of this cluster, over all of its tiles
-    for (int r = 0; mx_snake(r, cluster, nclusters) < total; ++r) n += k_stages;
-    // the stage being multiplied, and the next one, whose scales are copied ahead
-    int stage = 0, kb = 0, acc = 0, nstage = 0, nkb = 0;
-    uint32_t acc_phase = 0, nphase = 0;
-    bool ok = true;
-    for (int i = -1; ok && i < n; ++i) {  // i = -1: only the first stage's scales
-      if (i >= 0 && kb == 0)
-        ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles);
-      if (ok && i + 1 < n)
-        ok = mbar_wait(&full[nstage], nphase, p.status, abort_flag, p.wait_cycles);
+      for (long long i = (issued > ring ? issued - ring : 0); i < issued; ++i)
+        mbar_wait_plain(&full[i % ring], (uint32_t)((i / ring) & 1), p.wait_cycles);
+  } else if ((warp == 1 || warp == X_EPI + 2) && leader) {
+    // ---------------- MMAs (warp 1) and scale copies (the last warp), leader only ----------------
+    const bool copier = warp != 1;
+    const int n = (t1 - t0) * k_stages;  // stages of this cluster, over all of its tiles
+    // ring stage, K step, column tile, set of A's slots
+    int stage = 0, kb = 0, col = t0 % p.n_tiles, group = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int i = 0; i < n; ++i) {
+      bool ok = true;
+      if (copier) {
+        ok = mbar_wait(&full[stage], phase, p.status, abort_flag, p.wait_cycles);
+      } else {
+        if (kb == 0)
+          ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag, p.wait_cycles);
+        ok = ok && mbar_wait(&sfull[stage], phase, p.status, abort_flag, p.wait_cycles);
+      }
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      if (elect_one()) {
-        if (i + 1 < n) {
-          const uint64_t sf = sdesc_scales(smem_u32(scales) + nstage * C::sf);
-          const uint32_t ca = tmem_base + X_SF_COL + 32 * nstage, cb = ca + 8;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {  // 128-wide K tiles; the last stage may have one
-            if (2 * nkb + j >= p.k_tiles) break;
-            tc_cp_scales(ca + 4 * j, sf + j * (kMx4TileBytes / 16));
-#pragma unroll
-            for (int q = 0; q < C::sfb; ++q)
-              tc_cp_scales(cb + 4 * C::sfb * j + 4 * q,
-                           sf + ((1 + q) * X_SF + j * kMx4TileBytes) / 16);
-          }
-        }
-        if (i >= 0) {
-          const uint64_t ad = sdesc_kmajor_sw128(smem_u32(tiles) + stage * C::ops);
-          const uint64_t bd = ad + X_A / 16;
-          const uint32_t ca = tmem_base + X_SF_COL + 32 * stage, cb = ca + 8;
-          const uint32_t d = tmem_base + (uint32_t)(acc * C::N);
+      const int slot = resident ? group * k_stages + kb : stage;
+      const uint32_t ca = tmem_base + C::sfa_col + 8 * slot;
+      const uint32_t cb = tmem_base + C::sfb_col + 8 * C::sfb * stage;
+      const bool two = 2 * kb + 1 < p.k_tiles;  // 128-wide K tiles; the last stage may have one
+      if (copier) {
+        const bool fresh = i < k_stages || col == 0 || !resident;
+        const uint64_t sa = sdesc_scales(smem_u32(ascale) + slot * X_SF);
+        const uint64_t sb = sdesc_scales(smem_u32(bscale) + stage * C::sfb * X_SF);
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (2 * kb + j >= p.k_tiles) break;
+            if (j == 1 && !two) break;
+            if (fresh) tc_cp_scales(ca + 4 * j, sa + j * (kMx4TileBytes / 16));
+#pragma unroll
+            for (int q = 0; q < C::sfb; ++q)
+              tc_cp_scales(cb + 4 * C::sfb * j + 4 * q, sb + (q * X_SF + j * kMx4TileBytes) / 16);
+          }
+          tc_commit_pair(&sfull[stage]);
+        }
+      } else {
+        const uint64_t ad = sdesc_kmajor_sw128(smem_u32(abuf) + slot * X_A);
+        const uint64_t bd = sdesc_kmajor_sw128(smem_u32(bbuf) + stage * C::b_bytes);
+        const uint32_t d = tmem_base + (uint32_t)(acc * C::N);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (j == 1 && !two) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q)  // 64 K (32 bytes, two scales) each
               tc_mma_mx4(d, ad + 2 * (2 * j + q), bd + 2 * (2 * j + q),
@@ -385,28 +419,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         }
       }
       __syncwarp();
-      if (i >= 0) {
-        if (++stage == X_STAGES) stage = 0;
-        if (++kb == k_stages) {
-          kb = 0;
-          if (++acc == C::nacc) {
-            acc = 0;
-            acc_phase ^= 1u;
-          }
-        }
+      if (++stage == ring) {
+        stage = 0;
+        phase ^= 1u;
       }
-      if (i + 1 < n) {
-        if (++nkb == k_stages) nkb = 0;
-        if (++nstage == X_STAGES) {
-          nstage = 0;
-          nphase ^= 1u;
+      if (++kb == k_stages) {
+        kb = 0;
+        if (++acc == C::nacc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+        if (++col == p.n_tiles) {
+          col = 0;
+          if (++group == groups) group = 0;
         }
       }
     }
-    if (elect_one()) tc_commit_pair(drain);
+    if (elect_one()) tc_commit_pair(&drain[copier]);
     __syncwarp();
-    mbar_wait_plain(drain, 0, p.wait_cycles);
-  } else if (warp >= 2) {
+    mbar_wait_plain(&drain[copier], 0, p.wait_cycles);
+  } else if (warp >= 2 && warp < X_EPI + 2) {
     // ---------------- epilogue (both CTAs) ----------------
     // GLU: 16 warps per tile, a quarter of the columns each.  DOWN: the two halves of the warps
     // take every second tile (accumulator), half of the columns each.
@@ -420,10 +452,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       return (GLU || tl.dummy) ? 0.0f : __ldg(p.row_weight + tl.row0 + sub * 32 + lane);
     };
     uint32_t acc_phase = 0;
-    int r = mine_acc, t = mx_snake(r, cluster, nclusters);
-    MxTile nx = mx_decode(p, max(0, min(t, total - 1)), tables, rank);
-    float wnx = (t < total) ? weight_of(nx) : 0.0f;
-    while (t < total) {
+    int t = t0 + mine_acc;
+    MxTile nx = mx_first(p, min(t, max(total - 1, 0)), tables, rank);
+    float wnx = (t < t1) ? weight_of(nx) : 0.0f;
+    while (t < t1) {
       const MxTile tl = nx;
       const float wr = wnx;
       const int row = tl.row0 + sub * 32 + lane;
@@ -444,10 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       __syncwarp();
       if (lane == 0)  // accumulator free: values in registers
         mbar_arrive_remote(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
-      r += C::nacc;
-      t = mx_snake(r, cluster, nclusters);
-      if (t < total) {
-        nx = mx_decode(p, t, tables, rank);
+      t += C::nacc;
+      if (t < t1) {
+        mx_step(p, nx, C::nacc, tables, rank);
         wnx = weight_of(nx);
       }
       if (tl.dummy) continue;
@@ -545,10 +576,6 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
   p.status = g.status;
   p.inject = take_inject_stall();
   p.wait_cycles = p.inject ? kInjectedWaitCycles : kWaitCycles;
-  // units whose A rows (2 x 128 x K / 2 bytes each) fill about 40 MB of L2 share B tiles
-  const long long per_unit = 2LL * XM * p.k_tiles * 64;
-  const long long group = (40LL << 20) / per_unit;
-  p.group = (int)(group < 1 ? 1 : group > 64 ? 64 : group);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k_mx4_gemm<GLU>, done, (int)MxCfg<GLU>::smem);
   if (e != cudaSuccess) return e;
@@ -565,10 +592,6 @@ cudaError_t launch_mx(const GemmProblem &g, MxParams &p, cudaStream_t st) {
     max_clusters = n;
   });
   const long long max_tiles = ((long long)g.nblk_cap / 2 + g.E) * p.n_tiles;
-  // t * ceil(2^32 / n) / 2^32 truncates to t / n while t * n < 2^32
-  p.n_magic = (p.n_tiles > 1 && max_tiles * p.n_tiles < (1LL << 32))
-                  ? (uint32_t)(((1ull << 32) + p.n_tiles - 1) / p.n_tiles)
-                  : 0u;
   const long long clusters = max_tiles < max_clusters ? max_tiles : max_clusters;
   return launch_pdl(k_mx4_gemm<GLU>, (int)(2 * clusters), X_THREADS, MxCfg<GLU>::smem, st, p);
 }
