@@ -333,7 +333,7 @@ Mx4Layout mx4_layout(const dmoe_dims *d) {
 int check_mx4_matrix(int64_t rows, int64_t cols) {
   if (rows < 1 || cols < DMOE_BLOCKING || cols % DMOE_BLOCKING != 0) return DMOE_ERR_SHAPE;
   // element offsets stay within 64 bits, column tiles within 32
-  return (rows <= (1LL << 40) && cols <= (1LL << 30) && rows <= (1LL << 60) / cols)
+  return (rows <= (1LL << 40) && cols <= (1LL << 23) && rows <= (1LL << 60) / cols)
              ? DMOE_OK
              : DMOE_ERR_TOO_LARGE;
 }

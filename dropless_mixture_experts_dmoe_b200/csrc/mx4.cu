@@ -19,25 +19,37 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   return v;
 }
 
+// Per half: the larger of two unsigned 16-bit values.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The two bf16 values of w times a power of two (bf16), in fp32: exact.
+__device__ __forceinline__ void scale_bf16x2(uint32_t w, uint16_t f, float &lo, float &hi) {
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, %3, %4;\n\tfma.rn.f32.bf16 %1, h, %3, %4;}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w), "h"(f), "f"(-0.0f));  // -0 keeps the sign of a zero
+}
+
 // One lane's 8 columns of a row: the elements, and (in every lane of the block's four) the
-// block's scale byte.  All lanes of the warp take part.
+// block's scale byte.  All lanes of the warp take part.  Magnitudes of bf16 values order like
+// their bits, two at a time.
 __device__ __forceinline__ uint32_t quantize8(uint4 q, uint32_t &scale) {
   const uint32_t *w = reinterpret_cast<const uint32_t *>(&q);
-  uint32_t m = 0u;  // the largest |x| as fp32 bits (integers order like magnitudes)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  scale = mx4_scale_byte(m);
-  if (scale == 255u) return 0u;
-  const float inv = mx4_inverse(scale);
+  uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                         max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  scale = mx4_scale_byte(max(m << 16, m & 0xFFFF0000u));
+  // the inverse scale 2^(127 - s) as bf16 (s <= 252)
+  const uint16_t inv = (uint16_t)((254u - min(scale, 253u)) << 7);
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]) * inv;
-    v[2 * i + 1] = bf16_hi(w[i]) * inv;
-  }
-  return mx4_pack8(v);
+  for (int i = 0; i < 4; ++i) scale_bf16x2(w[i], inv, v[2 * i], v[2 * i + 1]);
+  const uint32_t c = mx4_pack8(v);
+  return scale == 255u ? 0u : c;
 }
 
 // The scale bytes of a lane group's 16 lanes (128 columns: four blocks) as one word, in the
@@ -54,7 +66,8 @@ __device__ __forceinline__ uint32_t scale_word16(uint32_t scale, int lane) {
 //
 // src [rows, cols] bf16 -> codes [rows, cols / 2], scales in tiles.  A warp takes 256 columns (two
 // column tiles; the last pair of a row may be half) of the four rows, all four 16-byte loads of
-// a lane in flight at once; one row at a time measured 2.3x slower (bound by load latency).
+// a lane in flight at once (one row at a time: 202 us there and back for 65536 x 2048, bound by
+// load latency; in 64-bit item arithmetic 133 us, bound by its instructions).
 // Rows past `rows` of the last row tile get scale bytes 0.
 __global__ void __launch_bounds__(kMx4Threads)
     k_mx4_quantize(long long rows, int vpr, const uint4 *__restrict__ src,
@@ -63,19 +76,19 @@ __global__ void __launch_bounds__(kMx4Threads)
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int ct = vpr >> 4;  // column tiles; vpr = 16-byte vectors (8 columns) per row
-  const int S = (vpr + 31) >> 5;
-  const long long items = (rows + 127) / 128 * 32 * S;
-  const long long nw = (long long)gridDim.x * kMx4Warps;
-  for (long long it = (long long)blockIdx.x * kMx4Warps + (threadIdx.x >> 5); it < items;
-       it += nw) {
-    const long long lr = it / S;
-    const int v = (int)(it - lr * S) * 32 + lane;
+  const long long groups = (rows + 127) / 128 * 32;  // of four rows
+  const int v = blockIdx.y * 32 + lane;              // 256 columns per blockIdx.y
+  for (long long lr = (long long)blockIdx.x * kMx4Warps + (threadIdx.x >> 5); lr < groups;
+       lr += (long long)gridDim.x * kMx4Warps) {
     const long long r0 = (lr >> 5) * 128 + (lr & 31);
+    const uint4 *sp = src + r0 * vpr + v;
+    uint32_t *cp = codes + r0 * vpr + v;
     uint4 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long r = r0 + 32 * i;
-      q[i] = (v < vpr && r < rows) ? ld_stream(src + r * vpr + v) : make_uint4(0u, 0u, 0u, 0u);
+      q[i] = (v < vpr && r < rows) ? ld_stream(sp + (size_t)(32 * i) * vpr)
+                                   : make_uint4(0u, 0u, 0u, 0u);
     }
     uint32_t w[4];
 #pragma unroll
@@ -84,7 +97,7 @@ __global__ void __launch_bounds__(kMx4Threads)
       uint32_t sc;
       const uint32_t c = quantize8(q[i], sc);
       w[i] = (r < rows) ? scale_word16(sc, lane) : 0u;  // r is the same in the whole warp
-      if (v < vpr && r < rows) codes[r * vpr + v] = c;
+      if (v < vpr && r < rows) cp[(size_t)(32 * i) * vpr] = c;
     }
     if (v < vpr && (lane & 15) == 0)
       *reinterpret_cast<uint4 *>(scales + mx4_scale_word(r0, v >> 4, ct)) =
@@ -100,20 +113,19 @@ __global__ void __launch_bounds__(kMx4Threads)
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int ct = vpr >> 4;
-  const int S = (vpr + 31) >> 5;
-  const long long items = (rows + 127) / 128 * 32 * S;
-  const long long nw = (long long)gridDim.x * kMx4Warps;
-  for (long long it = (long long)blockIdx.x * kMx4Warps + (threadIdx.x >> 5); it < items;
-       it += nw) {
-    const long long lr = it / S;
-    const int v = (int)(it - lr * S) * 32 + lane;
-    if (v >= vpr) continue;
+  const long long groups = (rows + 127) / 128 * 32;
+  const int v = blockIdx.y * 32 + lane;
+  if (v >= vpr) return;
+  for (long long lr = (long long)blockIdx.x * kMx4Warps + (threadIdx.x >> 5); lr < groups;
+       lr += (long long)gridDim.x * kMx4Warps) {
     const long long r0 = (lr >> 5) * 128 + (lr & 31);
+    const uint32_t *cp = codes + r0 * vpr + v;
+    uint4 *dp = dst + r0 * vpr + v;
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long r = r0 + 32 * i;
-      c[i] = (r < rows) ? __ldg(codes + r * vpr + v) : 0u;
+      c[i] = (r < rows) ? __ldg(cp + (size_t)(32 * i) * vpr) : 0u;
     }
     const uint4 sw = __ldg(reinterpret_cast<const uint4 *>(scales + mx4_scale_word(r0, v >> 4, ct)));
     const uint32_t w[4] = {sw.x, sw.y, sw.z, sw.w};
@@ -128,7 +140,7 @@ __global__ void __launch_bounds__(kMx4Threads)
       uint32_t *dw = reinterpret_cast<uint32_t *>(&d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dw[j] = pack_bf16x2(f16_lo(o[j]) * s, f16_hi(o[j]) * s);
-      dst[r * vpr + v] = d;
+      dp[(size_t)(32 * i) * vpr] = d;
     }
   }
 }
@@ -209,19 +221,25 @@ static int mx4_grid(long long items, long long per_cta) {
   return (int)(g < 1 ? 1 : g);
 }
 
+// blockIdx.y: 256 columns; blockIdx.x strides over groups of four rows, eight per CTA.  (A grid's y
+// extent ends at 65535: 16.7 million columns, the limit that the entry points state.)
+static dim3 mx4_grid2(long long rows, long long cols) {
+  const long long y = (cols / 8 + 31) / 32;
+  long long x = (rows + 127) / 128 * 32 / kMx4Warps;
+  const long long cap = ((long long)device_sm_count() * 8 + y - 1) / y;
+  return dim3((unsigned)(x < cap ? x : cap), (unsigned)y);
+}
+
 cudaError_t launch_mx4_quantize(long long rows, long long cols, const void *src, void *codes,
                                 void *scales, cudaStream_t st) {
-  const long long items = (rows + 127) / 128 * 32 * ((cols / 8 + 31) / 32);
-  return launch_pdl(k_mx4_quantize, mx4_grid(items, kMx4Warps), kMx4Threads, 0, st, rows,
-                    (int)(cols / 8),
-                    static_cast<const uint4 *>(src), static_cast<uint32_t *>(codes),
-                    static_cast<uint8_t *>(scales));
+  return launch_pdl(k_mx4_quantize, mx4_grid2(rows, cols), kMx4Threads, 0, st, rows,
+                    (int)(cols / 8), static_cast<const uint4 *>(src),
+                    static_cast<uint32_t *>(codes), static_cast<uint8_t *>(scales));
 }
 
 cudaError_t launch_mx4_dequantize(long long rows, long long cols, const void *codes,
                                   const void *scales, void *dst, cudaStream_t st) {
-  const long long items = (rows + 127) / 128 * 32 * ((cols / 8 + 31) / 32);
-  return launch_pdl(k_mx4_dequantize, mx4_grid(items, kMx4Warps), kMx4Threads, 0, st, rows,
+  return launch_pdl(k_mx4_dequantize, mx4_grid2(rows, cols), kMx4Threads, 0, st, rows,
                     (int)(cols / 8), static_cast<const uint32_t *>(codes),
                     static_cast<const uint8_t *>(scales), static_cast<uint4 *>(dst));
 }

@@ -481,7 +481,7 @@ typedef struct {
  * the nearest e2m1 value to x / 2^(s - 127), ties to the even mantissa, saturated at +-6.  A
  * block that holds an inf or NaN gets the scale NaN and zero codes.  Scale bytes of the rows
  * that fill the last tile are written as 0. rows >= 1.  DMOE_ERR_SHAPE for
- * rows < 1 or cols not a multiple of 128, DMOE_ERR_TOO_LARGE past 2^40 rows or 2^30 columns. */
+ * rows < 1 or cols not a multiple of 128, DMOE_ERR_TOO_LARGE past 2^40 rows or 2^23 columns. */
 DMOE_API int dmoe_mx4_quantize(int64_t rows, int64_t cols, const void *src, const dmoe_mx4 *dst,
                                void *stream);
 /* src -> dst [rows, cols] bf16: element times scale.  Exact, except that a product beyond bf16's

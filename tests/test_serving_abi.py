@@ -56,7 +56,8 @@ def test_few_refusals(lib, mx4):
 def test_mx4_conversion_refusals(lib):
     m = B.dmoe_mx4(FAKE, FAKE)
     for rows, cols, code in ((0, 128, -2), (-1, 128, -2), (4, 0, -2), (4, 64, -2), (4, 200, -2),
-                             (2 ** 41, 128, -8), (4, 2 ** 31, -8), (2 ** 40, 2 ** 30, -8)):
+                             (2 ** 41, 128, -8), (4, 2 ** 31, -8), (4, 2 ** 24, -8),
+                             (2 ** 40, 2 ** 23, -8)):
         assert lib.dmoe_mx4_quantize(rows, cols, FAKE, ctypes.byref(m), None) == code
         assert lib.dmoe_mx4_dequantize(rows, cols, ctypes.byref(m), FAKE, None) == code
     for bad, code in ((None, -1), (B.dmoe_mx4(0, FAKE), -1), (B.dmoe_mx4(FAKE, 0), -1),
