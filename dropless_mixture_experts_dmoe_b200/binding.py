@@ -398,7 +398,11 @@ def _arg(name: str, t, shape: tuple, dtype, device: int) -> int:
 class Mx4:
     """A matrix, or a stack of expert matrices, in the microscaled 4-bit format (see dmoe_mx4 in
     include/dmoe.h): ``codes`` [..., rows, cols / 2] and ``scales`` [..., ceil(rows/128), cols/128,
-    32, 4, 4], contiguous uint8 tensors.  In a stack ``rows`` is a multiple of 128."""
+    32, 4, 4], contiguous uint8 tensors, fixed for the object's life.  In a stack ``rows`` is a
+    multiple of 128."""
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not (
@@ -409,7 +413,7 @@ class Mx4:
             raise ValueError(f"scales of codes {tuple(codes.shape)}: {tuple(scales.shape)}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales = codes, scales
         self._device = codes.get_device()
         self._c = dmoe_mx4(codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.byref(self._c)
@@ -463,27 +467,43 @@ def dmoe_mx4_dequantize(src: Mx4, dst, stream=None):
 
 class FewBuffers:
     """Device buffers of the few-token calls for one shape: ``top_experts`` [T,k] and ``weights``
-    [T,k] (outputs when logits are given, else inputs), ``status`` (starts at 0, bits are OR-ed
-    in) and the workspace ``ws``."""
+    [T,k] (outputs when logits are given, else inputs: copy the given routing into them),
+    ``status`` (starts at 0, bits are OR-ed in) and the workspace ``ws``."""
+
+    top_experts = property(lambda self: self._tensors[0])
+    weights = property(lambda self: self._tensors[1])
+    status = property(lambda self: self._tensors[2])
+    ws = property(lambda self: self._tensors[3])
 
     def __init__(self, dims: dmoe_dims, device="cuda"):
         n = dmoe_workspace_bytes(dims, WS_FEW)
         if n == 0:
             raise DMoEError(-2, "FewBuffers")
         self.dims = dims
-        self.top_experts = torch.empty((dims.T, dims.top_k), dtype=torch.int32, device=device)
-        self.weights = torch.empty((dims.T, dims.top_k), dtype=torch.float32, device=device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
-        self._args = (self.top_experts.data_ptr(), self.weights.data_ptr(),
-                      self.status.data_ptr(), self.ws.data_ptr(), n)
+        self._sizes = _sizes(dims)
+        self._tensors = (
+            torch.empty((dims.T, dims.top_k), dtype=torch.int32, device=device),
+            torch.empty((dims.T, dims.top_k), dtype=torch.float32, device=device),
+            torch.zeros(1, dtype=torch.int32, device=device),
+            torch.empty(n, dtype=torch.uint8, device=device))
+        self._device = self.ws.get_device()
+        self._args = (*(t.data_ptr() for t in self._tensors), n)
+
+    def args(self, device: int) -> tuple:
+        """Addresses of the buffers and the size of ws, on the current CUDA device."""
+        if self._device != device:
+            raise ValueError("the buffers must be on the current CUDA device; they are on "
+                             f"{self.ws.device}")
+        return self._args
+
+
+def _sizes(dims) -> tuple:
+    return dims.T, dims.hidden, dims.ffn, dims.num_experts, dims.top_k
 
 
 def _few_args(dims, x, logits, bufs, y, dev):
-    d = bufs.dims
-    if d is not dims and (d.T, d.hidden, d.ffn, d.num_experts, d.top_k) != (
-            dims.T, dims.hidden, dims.ffn, dims.num_experts, dims.top_k):
-        raise ValueError(f"the buffers are those of {d}, not of {dims}")
+    if bufs._sizes != _sizes(dims):
+        raise ValueError(f"the buffers are those of sizes {bufs._sizes}, not of {_sizes(dims)}")
     row = (dims.T, dims.hidden)
     return (_arg("x", x, row, torch.bfloat16, dev),
             None if logits is None else _arg("logits", logits, (dims.T, dims.num_experts),
@@ -497,12 +517,11 @@ def dmoe_forward_few(dims: dmoe_dims, x, logits, w1, w3, w2, bufs: FewBuffers, y
     dev = _device()
     xp, lp, yp = _few_args(dims, x, logits, bufs, y, dev)
     E, h, f, bf = dims.num_experts, dims.hidden, dims.ffn, torch.bfloat16
-    top, weights, status, ws, n = bufs._args
-    _check(load().dmoe_forward_few(ctypes.byref(dims), xp, lp, _arg("w1", w1, (E, f, h), bf, dev),
-                                   _arg("w3", w3, (E, f, h), bf, dev),
-                                   _arg("w2", w2, (E, h, f), bf, dev), top, weights, yp, status,
-                                   ws, n, _stream(stream)),
-           "dmoe_forward_few")
+    w = (_arg("w1", w1, (E, f, h), bf, dev), _arg("w3", w3, (E, f, h), bf, dev),
+         _arg("w2", w2, (E, h, f), bf, dev))
+    top, weights, status, ws, n = bufs.args(dev)
+    _check(load().dmoe_forward_few(ctypes.byref(dims), xp, lp, *w, top, weights, yp, status, ws, n,
+                                   _stream(stream)), "dmoe_forward_few")
 
 
 def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, bufs: FewBuffers,
@@ -511,12 +530,10 @@ def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, 
     dev = _device()
     xp, lp, yp = _few_args(dims, x, logits, bufs, y, dev)
     E, h, f = dims.num_experts, dims.hidden, dims.ffn
-    top, weights, status, ws, n = bufs._args
-    _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), xp, lp, w1.arg("w1", (E, f, h), dev),
-                                       w3.arg("w3", (E, f, h), dev),
-                                       w2.arg("w2", (E, h, f), dev), top, weights, yp, status,
-                                       ws, n, _stream(stream)),
-           "dmoe_mx4_forward_few")
+    w = (w1.arg("w1", (E, f, h), dev), w3.arg("w3", (E, f, h), dev), w2.arg("w2", (E, h, f), dev))
+    top, weights, status, ws, n = bufs.args(dev)
+    _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), xp, lp, *w, top, weights, yp, status,
+                                       ws, n, _stream(stream)), "dmoe_mx4_forward_few")
 
 
 class Mx4Buffers:
@@ -545,6 +562,9 @@ def dmoe_mx4_forward(dims: dmoe_dims, x, w1: Mx4, w3: Mx4, w2: Mx4, smap: Sparse
     """y [T,h] = the layer with every product in the microscaled 4-bit format (inference)."""
     E, h, f, row = dims.num_experts, dims.hidden, dims.ffn, (dims.T, dims.hidden)
     dev = _device()
+    if _sizes(smap.dims) != _sizes(dims):
+        raise ValueError(f"the map is that of {smap.dims}, not of {dims}")
+    _arg("smap.status", smap.status, (1,), torch.int32, dev)
     _check(load().dmoe_mx4_forward(ctypes.byref(dims), _arg("x", x, row, torch.bfloat16, dev),
                                    w1.arg("w1", (E, f, h), dev), w3.arg("w3", (E, f, h), dev),
                                    w2.arg("w2", (E, h, f), dev), ctypes.byref(smap.c),

@@ -147,6 +147,31 @@ def test_binding_checks_tensors_on_the_host():
         B.dmoe_mx4_dequantize(q1, w1)
 
 
+def test_buffers_of_the_serving_calls_are_fixed():
+    """Their addresses are taken once: a replaced tensor or a changed size is refused."""
+    d = B.make_dims(4, 256, 128, 8, 2)
+    few = B.FewBuffers(d, device="cpu")
+    for name in ("top_experts", "weights", "status", "ws"):
+        with pytest.raises(AttributeError):
+            setattr(few, name, getattr(few, name).clone())
+    q = B.Mx4.empty(8, 128, 256, device="cpu")
+    for name in ("codes", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, getattr(q, name).clone())
+    d.T = 5
+    with pytest.raises(ValueError, match="buffers"):
+        B.dmoe_forward_few(d, FAKE, FAKE, FAKE, FAKE, FAKE, few, FAKE)
+    d.T = 4
+    with pytest.raises(ValueError, match="the buffers must be on"):
+        B.dmoe_forward_few(d, FAKE, FAKE, FAKE, FAKE, FAKE, few, FAKE)
+    m = B.Mx4Buffers(d, device="cpu")
+    w = (q, q, B.Mx4.empty(8, 256, 128, device="cpu"))
+    with pytest.raises(ValueError, match="the map is"):
+        B.dmoe_mx4_forward(B.make_dims(5, 256, 128, 8, 2), FAKE, *w, m.map, FAKE, m.ws)
+    with pytest.raises(ValueError, match="smap.status"):
+        B.dmoe_mx4_forward(d, FAKE, *w, m.map, FAKE, m.ws)
+
+
 def test_weights_too_tall(lib):
     """Rows of the stacked weights past 31 bits."""
     d = B.make_dims(4, 2 ** 22, 128, 1024, 2)
