@@ -23,10 +23,15 @@
 //   warp 1      leader only: four MMAs of 64 K per stage.  One warp that did both took 1000
 //               clocks a stage, where the MMAs take 512
 //   warps 2..17 epilogue: a warp takes 32 rows and 64 accumulator columns
+//               (eight warps with twice the columns measured level)
 // Tensor memory: 256 accumulator columns, and 32 columns of scales per stage, which are
 // rewritten only after the stage's MMAs are done.  Two GLU accumulators and scales do not fit in
 // 512 columns; instead an epilogue warp takes its 64 columns into registers at once and releases
 // the accumulator before it converts and stores them.
+//
+// Measured at T = 4096, hidden 2048, ffn 1024, E = 64, top-8 (412 GFLOP): GLU 78 us, DOWN 67 us; in
+// counters the tensor pipe is 55 % and 28 % active, DRAM 57 % and 48 % busy.  GLU waits on its
+// one accumulator's hand-over between tiles, DOWN on the stores of Y_pad.
 //
 // Every mbarrier wait is bounded; on expiry the kernel sets DMOE_STATUS_TIMEOUT, raises an
 // abort flag for the other roles of its CTA, drains what it issued and returns.
@@ -180,7 +185,7 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
 
 // One lane of a converged warp.  The producer and MMA warps run their loops as whole warps and
 // elect the lane only around the instructions: their operands then stay in uniform registers
-// (a loop of one lane moved every operand over, about 90 clocks an instruction).
+// (as a loop of one lane the MMA warp took about 900 clocks a stage).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"

@@ -490,7 +490,9 @@ DMOE_API int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src
                                  void *stream);
 
 /* dmoe_forward_few over expert weights in the format (w1, w3 as [E * f, h], w2 as [E * h, f]);
- * x and the sums keep their precision, only the weights have four bits. */
+ * x and the sums keep their precision, only the weights have four bits.  A row of x is scaled by a
+ * power of two that takes its largest value to 2^15, so weights beyond 2^100 can overflow the
+ * fp32 sums where the true result does not. */
 DMOE_API int dmoe_mx4_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
                                   const dmoe_mx4 *w1, const dmoe_mx4 *w3, const dmoe_mx4 *w2,
                                   int32_t *top_experts, float *weights, void *y,
