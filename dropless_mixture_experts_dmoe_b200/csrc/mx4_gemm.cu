@@ -16,8 +16,8 @@
 //               the scale tiles of all rows of B (each SM of the pair multiplies by all of them);
 //               and its 128 rows of A (16 KB) with their scales: GLU for every stage (a ring of six;
 //               a stage's round trip is about 4000 clocks, its MMAs 512), DOWN (K up to 1024) once
-//               per unit, which leaves room for a ring of nine stages of B.  Each pair takes a
-//               contiguous share of the tiles, a unit's columns in a row
+//               per unit, which leaves room for a ring of nine stages of B.  A pair takes a unit's
+//               columns in a row
 //   warp 18     leader only: tcgen05.cp of a stage's scale tiles into tensor memory (512-byte
 //               tiles, each 32 lanes x 4 columns repeated for the four lane groups)
 //   warp 1      leader only: four MMAs of 64 K per stage.  One warp that did both took 1000
@@ -29,9 +29,9 @@
 // 512 columns; instead an epilogue warp takes its 64 columns into registers at once and releases
 // the accumulator before it converts and stores them.
 //
-// Measured at T = 4096, hidden 2048, ffn 1024, E = 64, top-8 (412 GFLOP): GLU 78 us, DOWN 67 us; in
-// counters the tensor pipe is 55 % and 28 % active, DRAM 57 % and 48 % busy.  GLU waits on its
-// one accumulator's hand-over between tiles, DOWN on the stores of Y_pad.
+// Measured at T = 4096, hidden 2048, ffn 1024, E = 64, top-8 (412 GFLOP): GLU 69 us, DOWN 67 us; without
+// the epilogue's work 64 and 59, without MMAs either 60 and 57: what bounds both is the turn of the
+// ring (loads, scale copies, MMAs, release), not the tensor pipe or the stores.
 //
 // Every mbarrier wait is bounded; on expiry the kernel sets DMOE_STATUS_TIMEOUT, raises an
 // abort flag for the other roles of its CTA, drains what it issued and returns.
@@ -102,6 +102,26 @@ struct MxParams {
 struct MxTile {
   int vu, n, e, row0;
   bool dummy;
+  bool first;  // of its unit on this cluster
+};
+
+// A cluster's tiles, in order: as many whole units as every cluster can have, one from each round
+// of `clusters` neighbouring units, so that clusters at work on the same expert share its
+// weights in L2 (with contiguous shares of all tiles, units of an expert were far apart in time: the
+// first product of the fine-grained layer took 78 us, now 69); then a contiguous share [r0, r0 + count - whole) of the remaining units' tiles.
+struct MxShare {
+  int cluster, clusters, n_tiles;
+  int whole, count;  // tiles of whole units, of all
+  int rest, r0;      // first of the remaining units; first tile from there on
+  __device__ __forceinline__ MxShare(int c, int nc, int units, int nt)
+      : cluster(c), clusters(nc), n_tiles(nt) {
+    const int rounds = units / nc;
+    rest = rounds * nc;
+    whole = rounds * nt;
+    const int tiles = (units - rest) * nt;  // nt times fewer than nc
+    r0 = (int)((long long)c * tiles / nc);
+    count = whole + (int)((long long)(c + 1) * tiles / nc) - r0;
+  }
 };
 
 // The schedule's tables in shared memory, [E + 1] each: units and row blocks before expert e.
@@ -123,23 +143,15 @@ __device__ __forceinline__ void mx_unit(const MxParams &p, MxTile &tl, const MxT
   tl.row0 = (tl.dummy ? p.nblk_cap : b) * XM;  // past the last row: loads read zeros
 }
 
-// `by` tiles on: the columns of a unit first, then the next unit.
-__device__ __forceinline__ void mx_step(const MxParams &p, MxTile &tl, int by, const MxTables &tb,
-                                        uint32_t rank) {
-  tl.n += by;
-  if (tl.n < p.n_tiles) return;
-  while (tl.n >= p.n_tiles) {
-    tl.n -= p.n_tiles;
-    ++tl.vu;
-  }
-  mx_unit(p, tl, tb, rank);
-}
-
-__device__ __forceinline__ MxTile mx_first(const MxParams &p, int t, const MxTables &tb,
-                                           uint32_t rank) {
+// The cluster's i-th tile.
+__device__ __forceinline__ MxTile mx_tile(const MxParams &p, const MxShare &sh, int i,
+                                          const MxTables &tb, uint32_t rank) {
   MxTile tl;
-  tl.vu = t / p.n_tiles;
-  tl.n = t - tl.vu * p.n_tiles;
+  const bool whole = i < sh.whole;
+  const int j = whole ? i : sh.r0 + i - sh.whole, u = j / sh.n_tiles;
+  tl.n = j - u * sh.n_tiles;
+  tl.vu = whole ? u * sh.clusters + sh.cluster : sh.rest + u;
+  tl.first = tl.n == 0 || i == 0 || i == sh.whole;
   mx_unit(p, tl, tb, rank);
   return tl;
 }
@@ -301,10 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   cluster_sync_all();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  // this cluster's tiles: a contiguous share of all
-  const int total = ustart[p.E] * p.n_tiles;
-  const int t0 = (int)((long long)cluster * total / nclusters);
-  const int t1 = (int)((long long)(cluster + 1) * total / nclusters);
+  const MxShare share(cluster, nclusters, ustart[p.E], p.n_tiles);
+  const int count = share.count;
   const int k_stages = (p.k_tiles + 1) / 2;
   // DOWN: A stays in its slots while the unit's columns pass, in `groups` sets of slots by turns.
   // GLU, and a K too long for the slots: A passes through with B, stage by stage.
@@ -320,10 +330,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    MxTile tl = mx_first(p, min(t0, max(total - 1, 0)), tables, rank);
-    for (int t = t0; ok && t < t1; ++t) {
-      const bool fresh = t == t0 || tl.n == 0 || !resident;  // A has to be loaded
-      if (t != t0 && tl.n == 0 && ++group == groups) group = 0;
+    MxTile tl;
+    if (count > 0) tl = mx_tile(p, share, 0, tables, rank);
+    for (int t = 0; ok && t < count; ++t) {
+      const bool fresh = tl.first || !resident;  // A has to be loaded
+      if (t > 0 && tl.first && ++group == groups) group = 0;
       // B rows: this CTA's half; scale row tiles of all of B
       const int brow =
           GLU ? tl.e * p.f + tl.n * 128 : tl.e * p.h + tl.n * 128 + (int)rank * 64;
@@ -356,7 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
             tma_load_2d_pair(ascale + slot * X_SF, &p.tsa, bar, 0, sa0 + 2 * kb);
           }
         }
-        if (kb == 0) mx_step(p, tl, 1, tables, rank);  // the next tile, while this one loads
+        if (kb == 0 && t + 1 < count)  // the next tile, while this one loads
+          tl = mx_tile(p, share, t + 1, tables, rank);
         ++issued;
         if (++stage == ring) {
           stage = 0;
@@ -371,9 +383,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   } else if ((warp == 1 || warp == X_EPI + 2) && leader) {
     // ---------------- MMAs (warp 1) and scale copies (the last warp), leader only ----------------
     const bool copier = warp != 1;
-    const int n = (t1 - t0) * k_stages;  // stages of this cluster, over all of its tiles
-    // ring stage, K step, column tile, set of A's slots
-    int stage = 0, kb = 0, col = t0 % p.n_tiles, group = 0, acc = 0;
+    const int n = count * k_stages;  // stages of this cluster, over all of its tiles
+    // ring stage, K step, tile and its column, set of A's slots
+    int stage = 0, kb = 0, t = 0, col = share.whole > 0 ? 0 : share.r0 % p.n_tiles, group = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     for (int i = 0; i < n; ++i) {
       bool ok = true;
@@ -391,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       const uint32_t cb = tmem_base + C::sfb_col + 8 * C::sfb * stage;
       const bool two = 2 * kb + 1 < p.k_tiles;  // 128-wide K tiles; the last stage may have one
       if (copier) {
-        const bool fresh = i < k_stages || col == 0 || !resident;
+        const bool fresh = t == 0 || col == 0 || t == share.whole || !resident;
         const uint64_t sa = sdesc_scales(smem_u32(ascale) + slot * X_SF);
         const uint64_t sb = sdesc_scales(smem_u32(bscale) + stage * C::sfb * X_SF);
         if (elect_one()) {
@@ -438,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
           col = 0;
           if (++group == groups) group = 0;
         }
+        if (++t == share.whole) col = share.r0 % p.n_tiles;
       }
     }
     if (elect_one()) tc_commit_pair(&drain[copier]);
@@ -457,10 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       return (GLU || tl.dummy) ? 0.0f : __ldg(p.row_weight + tl.row0 + sub * 32 + lane);
     };
     uint32_t acc_phase = 0;
-    int t = t0 + mine_acc;
-    MxTile nx = mx_first(p, min(t, max(total - 1, 0)), tables, rank);
-    float wnx = (t < t1) ? weight_of(nx) : 0.0f;
-    while (t < t1) {
+    int t = mine_acc;
+    MxTile nx;
+    float wnx = 0.0f;
+    if (t < count) {
+      nx = mx_tile(p, share, t, tables, rank);
+      wnx = weight_of(nx);
+    }
+    while (t < count) {
       const MxTile tl = nx;
       const float wr = wnx;
       const int row = tl.row0 + sub * 32 + lane;
@@ -482,8 +499,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       if (lane == 0)  // accumulator free: values in registers
         mbar_arrive_remote(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
       t += C::nacc;
-      if (t < t1) {
-        mx_step(p, nx, C::nacc, tables, rank);
+      if (t < count) {
+        nx = mx_tile(p, share, t, tables, rank);
         wnx = weight_of(nx);
       }
       if (tl.dummy) continue;
