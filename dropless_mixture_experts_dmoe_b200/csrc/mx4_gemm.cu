@@ -156,6 +156,17 @@ __device__ __forceinline__ MxTile mx_tile(const MxParams &p, const MxShare &sh, 
   return tl;
 }
 
+// ... from tl, the one `by` tiles before it.
+__device__ __forceinline__ void mx_next(const MxParams &p, const MxShare &sh, MxTile &tl, int i,
+                                        int by, const MxTables &tb, uint32_t rank) {
+  if (tl.n + by < sh.n_tiles && (i < sh.whole || i - by >= sh.whole)) {  // of the same unit
+    tl.n += by;
+    tl.first = false;
+  } else {
+    tl = mx_tile(p, sh, i, tb, rank);
+  }
+}
+
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
   // 32 rows of 16 bytes, eight rows (128 B) per core matrix, no swizzle
   uint64_t d = 0;
@@ -368,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
           }
         }
         if (kb == 0 && t + 1 < count)  // the next tile, while this one loads
-          tl = mx_tile(p, share, t + 1, tables, rank);
+          mx_next(p, share, tl, t + 1, 1, tables, rank);
         ++issued;
         if (++stage == ring) {
           stage = 0;
@@ -500,8 +511,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         mbar_arrive_remote(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
       t += C::nacc;
       if (t < count) {
-        nx = mx_tile(p, share, t, tables, rank);
-        wnx = weight_of(nx);
+        const int vu = nx.vu;
+        mx_next(p, share, nx, t, C::nacc, tables, rank);
+        if (nx.vu != vu) wnx = weight_of(nx);
       }
       if (tl.dummy) continue;
       if (GLU) {
