@@ -295,9 +295,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     prefetch_tmap(&p.tsb[0]);
     prefetch_tmap(&p.tsb[1]);
   }
-  pdl_wait();  // the next kernel is released as this grid's CTAs exit
+  // GLU: the gather lets this kernel start after its own wait, so the map is complete; only the
+  // producer waits for the gather's rows.  (The next kernel is released as this grid's CTAs exit.)
+  if (!GLU) pdl_wait();
   for (int e = threadIdx.x; e < p.E; e += X_THREADS) {
-    const int end = p.padded_bins[e] / XM, first = (e > 0) ? p.padded_bins[e - 1] / XM : 0;
+    const int end = __ldcg(p.padded_bins + e) / XM;
+    const int first = (e > 0) ? __ldcg(p.padded_bins + e - 1) / XM : 0;
     ustart[e + 1] = (end - first + 1) / 2;
     bstart[e + 1] = end;
   }
@@ -343,6 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     bool ok = true;
     MxTile tl;
     if (count > 0) tl = mx_tile(p, share, 0, tables, rank);
+    if (GLU) pdl_wait();
     for (int t = 0; ok && t < count; ++t) {
       const bool fresh = tl.first || !resident;  // A has to be loaded
       if (t > 0 && tl.first && ++group == groups) group = 0;
