@@ -10,6 +10,7 @@ the step entry points) and take torch tensors where the C call takes device poin
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -383,6 +384,12 @@ def _device() -> int:
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
+def _stream_on(device: int, stream) -> int | None:
+    """_stream for callers that have the current device."""
+    return (torch._C._cuda_getCurrentRawStream(device) if stream is None and device >= 0 else
+            _stream(stream))
+
+
 def _arg(name: str, t, shape: tuple, dtype, device: int) -> int:
     """Address of an argument of the serving calls: a contiguous tensor of this shape and type on
     the current CUDA device (a raw device address is passed on as it is)."""
@@ -415,6 +422,7 @@ class Mx4:
             raise ValueError("codes and scales must be on one device")
         self._codes, self._scales = codes, scales
         self._device = codes.get_device()
+        self._size = (math.prod(self.shape[:-1]), self.shape[-1])
         self._c = dmoe_mx4(codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.byref(self._c)
 
@@ -440,29 +448,22 @@ class Mx4:
                    torch.empty(scales, dtype=torch.uint8, device=device))
 
 
-def _rows_cols(shape):
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    return rows, shape[-1]
-
-
 def dmoe_mx4_quantize(src, dst: Mx4, stream=None):
     """dst = src (bf16, the shape of dst) in the microscaled 4-bit format."""
-    rows, cols = _rows_cols(dst.shape)
+    rows, cols = dst._size
     dev = _device()
     _check(load().dmoe_mx4_quantize(rows, cols, _arg("src", src, dst.shape, torch.bfloat16, dev),
-                                    dst.arg("dst", dst.shape, dev), _stream(stream)),
+                                    dst.arg("dst", dst.shape, dev), _stream_on(dev, stream)),
            "dmoe_mx4_quantize")
 
 
 def dmoe_mx4_dequantize(src: Mx4, dst, stream=None):
     """dst (bf16) = the values of src."""
-    rows, cols = _rows_cols(src.shape)
+    rows, cols = src._size
     dev = _device()
     _check(load().dmoe_mx4_dequantize(rows, cols, src.arg("src", src.shape, dev),
                                       _arg("dst", dst, src.shape, torch.bfloat16, dev),
-                                      _stream(stream)), "dmoe_mx4_dequantize")
+                                      _stream_on(dev, stream)), "dmoe_mx4_dequantize")
 
 
 class FewBuffers:
@@ -521,7 +522,7 @@ def dmoe_forward_few(dims: dmoe_dims, x, logits, w1, w3, w2, bufs: FewBuffers, y
          _arg("w2", w2, (E, h, f), bf, dev))
     top, weights, status, ws, n = bufs.args(dev)
     _check(load().dmoe_forward_few(ctypes.byref(dims), xp, lp, *w, top, weights, yp, status, ws, n,
-                                   _stream(stream)), "dmoe_forward_few")
+                                   _stream_on(dev, stream)), "dmoe_forward_few")
 
 
 def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, bufs: FewBuffers,
@@ -533,7 +534,7 @@ def dmoe_mx4_forward_few(dims: dmoe_dims, x, logits, w1: Mx4, w3: Mx4, w2: Mx4, 
     w = (w1.arg("w1", (E, f, h), dev), w3.arg("w3", (E, f, h), dev), w2.arg("w2", (E, h, f), dev))
     top, weights, status, ws, n = bufs.args(dev)
     _check(load().dmoe_mx4_forward_few(ctypes.byref(dims), xp, lp, *w, top, weights, yp, status,
-                                       ws, n, _stream(stream)), "dmoe_mx4_forward_few")
+                                       ws, n, _stream_on(dev, stream)), "dmoe_mx4_forward_few")
 
 
 class Mx4Buffers:
@@ -570,7 +571,7 @@ def dmoe_mx4_forward(dims: dmoe_dims, x, w1: Mx4, w3: Mx4, w2: Mx4, smap: Sparse
                                    w2.arg("w2", (E, h, f), dev), ctypes.byref(smap.c),
                                    _arg("y", y, row, torch.bfloat16, dev),
                                    _arg("ws", ws, ws.shape, ws.dtype, dev),
-                                   ws.numel() * ws.element_size(), _stream(stream)),
+                                   ws.numel() * ws.element_size(), _stream_on(dev, stream)),
            "dmoe_mx4_forward")
 
 
