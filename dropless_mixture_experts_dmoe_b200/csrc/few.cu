@@ -301,15 +301,18 @@ struct FewCfg {
   static constexpr int fixed = 1024 + o_lists;  // the ring starts on a 1024-byte boundary
   static_assert(w_mat % 1024 == 0 && (!MX4 || DOWN || outs % 32 == 0), "boxes, whole blocks of H");
   static_assert(2 * P * 8 <= 112, "barriers");
+  static_assert(P * stage >= 16 * DMOE_MAX_EXPERTS, "masks");
 };
 
 // Bytes of the expert lists: entries [n] (j | token << 16), a factor of each [n] (DOWN: its
-// weight; GLU with 4-bit weights: the scale of its token's x), starts [E + 1], experts in use
-// (uint16); and with the routing done in the kernel the experts and weights [n].
+// weight; GLU with 4-bit weights: the scale of its token's x), a word per expert, groups of
+// up to 8 NT entries of one expert (at most one per expert in use and one per 8 entries, and where
+// the last one ends); and with the
+// routing done in the kernel the experts and weights [n].
 __host__ __device__ inline size_t few_list_bytes(const FewParams &p) {
   const int n = p.T * p.k;
-  const size_t a = (size_t)n * (p.logits ? 16 : 8) + (size_t)(p.E + 1) * 4 +
-                   (size_t)(p.E < n ? p.E : n) * 2;
+  const size_t a = (size_t)n * (p.logits ? 16 : 8) + (size_t)p.E * 4 +
+                   (size_t)((p.E < n ? p.E : n) + n / 8 + 1) * 4;
   return (a + 15) / 16 * 16;
 }
 
@@ -319,7 +322,7 @@ struct FewLists {
   int32_t *top;    // the routing, if this kernel does it
   float *weights;
   int *start;
-  uint16_t *act;
+  uint32_t *act;  // expert | first entry << 16
   __device__ __forceinline__ FewLists(uint8_t *base, const FewParams &p) {
     const int n = p.T * p.k, routed = p.logits ? n : 0;
     ent = reinterpret_cast<uint32_t *>(base);
@@ -327,7 +330,7 @@ struct FewLists {
     top = reinterpret_cast<int32_t *>(fac + n);
     weights = reinterpret_cast<float *>(top + routed);
     start = reinterpret_cast<int *>(weights + routed);
-    act = reinterpret_cast<uint16_t *>(start + p.E + 1);
+    act = reinterpret_cast<uint32_t *>(start + p.E);
   }
 };
 
@@ -354,11 +357,53 @@ __device__ __forceinline__ float few_weight(const FewParams &p, const FewLists &
   return w;
 }
 
-// The experts in use, in increasing order, and their entries: start[e] .. start[e + 1] in ent.
-// Returns the number of experts in use.  An entry's place in its expert's list decides only
-// which column of the product it is, so the order the atomics give does not show in any result.
+// Entry j of expert e takes place `at` of the lists.
 template <class C>
-__device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, int *s_act) {
+__device__ __forceinline__ void few_put(const FewParams &p, const FewLists &l, int j, int e,
+                                        int at) {
+  const int t = j / p.k;
+  l.ent[at] = (uint32_t)j | ((uint32_t)t << 16);
+  // 4-bit products come out halved (see blocks())
+  if (C::DOWN)
+    l.fac[at] = few_weight(p, l, j, e) * (C::MX4 ? 0.5f : 1.0f);
+  else if (C::MX4)
+    l.fac[at] = 0.5f * __ldcg(p.xscale + t);
+}
+
+// The lists of up to 32 entries, by one warp: places by counting smaller keys (expert, entry).
+// One token, E = 128, top-8: 13.9 us, 16.4 with the lists for any number.
+template <class C>
+__device__ __forceinline__ int few_lists32(const FewParams &p, const FewLists &l, int lane) {
+  const int n = p.T * p.k;
+  const int e = lane < n ? few_entry(p, l, lane) : -1;
+  const uint32_t key = e < 0 ? 0xFFFFFFFFu : (uint32_t)(e << 5 | lane);
+  int at = 0, first = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t o = __shfl_sync(0xFFFFFFFFu, key, i);
+    at += o < key;
+    first += (o >> 5) < (key >> 5);
+  }
+  const bool head = e >= 0 && (at - first) % (8 * C::NT) == 0;  // of a group
+  const uint32_t head_key = head ? key : 0xFFFFFFFFu;
+  int group = 0;
+  for (int i = 0; i < n; ++i) group += __shfl_sync(0xFFFFFFFFu, head_key, i) < key;
+  if (e >= 0) few_put<C>(p, l, lane, e, at);
+  if (head) l.act[group] = (uint32_t)e | ((uint32_t)at << 16);
+  const int groups = __popc(__ballot_sync(0xFFFFFFFFu, head));
+  const int total = __popc(__ballot_sync(0xFFFFFFFFu, e >= 0));
+  if (lane == 0) l.act[groups] = (uint32_t)total << 16;
+  return groups;
+}
+
+// The experts in use, in increasing order, in groups of up to 8 NT entries, and their entries,
+// one group's behind another's.  Returns the number of groups.  Where an expert may have more
+// than one group, its entries go by token, so that every CTA makes the same groups: by the tokens
+// of each expert as four words of bits (`mask`, in place of the stages, which are not in use yet).
+// Where it has one, an entry's place decides only which column of the product it is, and the
+// order that atomics give, which is quicker, does not show in any result.
+template <class C>
+__device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, int *s_act,
+                                         uint32_t *mask) {
   constexpr int THREADS = C::threads;
   const int n = p.T * p.k, lane = threadIdx.x & 31;
   int *start = l.start;
@@ -380,32 +425,62 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
         set_status(p.status, DMOE_STATUS_NONFINITE_LOGITS);
     }
   }
-  for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = 0;
+  if (n <= 32) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const int groups = few_lists32<C>(p, l, lane);
+      if (lane == 0) *s_act = groups;
+    }
+    __syncthreads();
+    return *s_act;
+  }
+  const bool by_token = p.T > 8 * C::NT;
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    if (by_token)
+      *reinterpret_cast<uint4 *>(mask + 4 * e) = make_uint4(0u, 0u, 0u, 0u);
+    else
+      start[e] = 0;
+  }
   __syncthreads();
   for (int j = threadIdx.x; j < n; j += THREADS) {
     const int e = few_entry(p, l, j);
-    if (e >= 0) atomicAdd(&start[e], 1);
+    if (e < 0) continue;
+    if (by_token)
+      atomicOr(&mask[4 * e + (j / p.k >> 5)], 1u << (j / p.k & 31));
+    else
+      atomicAdd(&start[e], 1);
   }
   __syncthreads();
-  if (threadIdx.x < 32) {  // ends of the lists (the entries are filled in from the back)
+  if (threadIdx.x < 32) {
     int carry = 0, na = 0;
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
-      const int c = (e < p.E) ? start[e] : 0;
-      const unsigned on = __ballot_sync(0xFFFFFFFFu, c > 0);
-      int v = c;
+      int c = 0;
+      if (e < p.E) {
+        if (by_token) {
+          const uint4 m = *reinterpret_cast<const uint4 *>(mask + 4 * e);
+          c = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+        } else {
+          c = start[e];
+        }
+      }
+      const int groups = (c + 8 * C::NT - 1) / (8 * C::NT);
+      int v = c | (groups << 16);  // both sums at once (at most 4096 each)
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, v, off);
         if (lane >= off) v += u;
       }
-      if (c > 0) l.act[na + __popc(on & ((1u << lane) - 1u))] = (uint16_t)e;
-      if (e < p.E) start[e] = carry + v;
-      na += __popc(on);
-      carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+      const int end = carry + (v & 0xFFFF), g1 = na + (v >> 16);
+      for (int g = 0; g < groups; ++g)
+        l.act[g1 - groups + g] = (uint32_t)e | ((uint32_t)(end - c + 8 * C::NT * g) << 16);
+      if (e < p.E) start[e] = by_token ? end - c : end;  // else filled in from the back
+      v = __shfl_sync(0xFFFFFFFFu, v, 31);
+      carry += v & 0xFFFF;
+      na += v >> 16;
     }
     if (lane == 0) {
-      start[p.E] = carry;
+      l.act[na] = (uint32_t)carry << 16;
       *s_act = na;
     }
   }
@@ -413,23 +488,32 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
   for (int j = threadIdx.x; j < n; j += THREADS) {
     const int e = few_entry(p, l, j);
     if (e < 0) continue;
-    const int at = atomicSub(&start[e], 1) - 1, t = j / p.k;
-    l.ent[at] = (uint32_t)j | ((uint32_t)t << 16);
-    // 4-bit products come out halved (see blocks())
-    if (C::DOWN)
-      l.fac[at] = few_weight(p, l, j, e) * (C::MX4 ? 0.5f : 1.0f);
-    else if (C::MX4)
-      l.fac[at] = 0.5f * __ldcg(p.xscale + t);
+    int at;
+    if (by_token) {
+      const int t = j / p.k;
+      at = start[e];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t m = mask[4 * e + w], below = (1u << (t & 31)) - 1u;
+        at += __popc(w < (t >> 5) ? m : w == (t >> 5) ? m & below : 0u);
+      }
+    } else {
+      at = atomicSub(&start[e], 1) - 1;
+    }
+    few_put<C>(p, l, j, e, at);
   }
-  __syncthreads();  // start[e] is now the first entry of e
+  if (by_token) fence_async_smem();  // the stages are the copies' again
+  __syncthreads();
   return *s_act;
 }
 
-// A place in a CTA's stream of stages: item (GLU: expert, row tile; DOWN: expert, part of K),
-// group of 8 NT entries, chunk of K.
+// A place in a CTA's stream of stages: item (GLU: group, row tile; DOWN: group, part of K), chunk
+// of K.  Groups of one expert are items of their own, which different CTAs take: with a CTA
+// that went through all groups of its expert, 96 tokens on a skewed router took 105 us, now 95.
 struct FewPos {
-  int a, b;             // index of the expert in use; tile or part
-  int e, n0, cnt;       // cnt: entries of the expert from n0 on (may exceed 8 NT)
+  int a, b;             // group; tile or part
+  int e, n0, cnt;       // expert, first entry, entries (8 NT at most, which its users say again:
+                        // the bound keeps loops over them out of the loading warp)
   int chunk, c0, c1;    // chunks [c0, c1) of K
   bool on;
 };
@@ -442,7 +526,7 @@ struct FewKernel {
   uint64_t *full, *empty;
   volatile int *abort_flag;
   int K, chunks, na;
-  int per, step;         // items per expert; items from one of this CTA's to its next
+  int per, step;         // items per group; items from one of this CTA's to its next
   int tile, part;        // DOWN: the CTA's row tile, chunks per part of K
 
   __device__ __forceinline__ void open(FewPos &q) const {
@@ -453,9 +537,10 @@ struct FewKernel {
     }
     q.on = q.a < na;
     if (!q.on) return;
-    q.e = l.act[q.a];
-    q.n0 = l.start[q.e];
-    q.cnt = l.start[q.e + 1] - q.n0;
+    const uint32_t g = l.act[q.a];
+    q.e = (int)(g & 0xFFFFu);
+    q.n0 = (int)(g >> 16);
+    q.cnt = (int)(l.act[q.a + 1] >> 16) - q.n0;
     q.c0 = C::DOWN ? q.b * part : 0;
     q.c1 = C::DOWN ? min(chunks, q.c0 + part) : chunks;
     q.chunk = q.c0;
@@ -469,12 +554,6 @@ struct FewKernel {
   }
   __device__ __forceinline__ void next(FewPos &q) const {
     if (++q.chunk < q.c1) return;
-    if (q.cnt > 8 * C::NT) {
-      q.n0 += 8 * C::NT;
-      q.cnt -= 8 * C::NT;
-      q.chunk = q.c0;
-      return;
-    }
     q.b += step;
     open(q);
   }
@@ -830,7 +909,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   const FewLists l(smem + C::o_lists, p);
   pdl_wait();
   pdl_trigger();
-  const int na = few_lists<C>(p, l, &s_act);
+  const int na = few_lists<C>(p, l, &s_act, reinterpret_cast<uint32_t *>(smem));
   const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.h,
                        (p.h + C::CH - 1) / C::CH, na, p.f / C::outs, (int)gridDim.x, 0, 0};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -881,9 +960,8 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
       });
 }
 
-// A cluster of G CTAs shares a row tile, each with every G-th of the experts in use (neighbouring
-// experts of a skewed router hold similar numbers of tokens) or parts of K; their sums are
-// added in rank order through distributed shared memory.
+// A cluster of G CTAs shares a row tile, each with every G-th of the groups or parts of K; their
+// sums are added in rank order through distributed shared memory.
 template <class C>
 __global__ void __launch_bounds__(C::threads, C::min_ctas)
     k_few_down(const __grid_constant__ FewParams p) {
@@ -896,7 +974,7 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
   float *ysum = reinterpret_cast<float *>(smem + C::o_lists + few_list_bytes(p));
   // Before the wait for k_few_glu: only what was complete when that kernel passed its own
   // wait (it lets this one start after that): the routing, and the caller's W2.
-  const int na = few_lists<C>(p, l, &s_act);
+  const int na = few_lists<C>(p, l, &s_act, reinterpret_cast<uint32_t *>(smem));
   const int G = p.groups, rank = (int)cluster_ctarank();
   const int chunks = (p.f + C::CH - 1) / C::CH;
   const FewKernel<C> k{p, l, smem_u32(smem), full, empty, abort_flag, p.f, chunks, na,
@@ -986,7 +1064,7 @@ cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   p.ws[1] = static_cast<const uint8_t *>(p.w3.scales);
   const size_t smem = C::fixed + few_list_bytes(p);
   const long long n = (long long)p.T * p.k;
-  const long long items = (n < p.E ? n : p.E) * (p.f / C::outs);
+  const long long items = ((n < p.E ? n : p.E) + n / (8 * C::NT)) * (p.f / C::outs);
   const long long ctas = few_places<C>(smem);
   return launch_pdl(k_few_glu<C>, (int)(items < ctas ? items : ctas), C::threads, smem, st, p);
 }
@@ -1088,13 +1166,13 @@ using BD8 = FewShape<8, 1, 64, 3, 1>;
 // weights again (from L2); one with fewer still has the larger tile's stages, fewer CTAs per SM
 // and rows to load.  The host knows T and the mean number of tokens per expert, mean = T k / E, not
 // the routing.
-//   4 bits: one tile up to 16 tokens (16 tokens, E = 64, top-8: 61 us, 69 with two), two up to a
-//     mean of 16 (64 tokens: 118 us, 136 with one, 114 to 156 with four), then four (128 tokens,
-//     E = 8, top-2, hidden 4096, ffn 14336: 670 us, 810 with two)
-//   bf16: up to 32 tokens one (32, E = 64, top-8: 140 us, 174 with two), from a mean of 4 on two
-//     (24, E = 16, top-4: 132 us, 142 with one); beyond that four, which a skewed router needs (96
-//     tokens, skewed: 117 us, 200 with one; 128 over E = 256: 306 us, 487 with one); from a mean of
-//     16 on eight (128 over E = 8: 740 us, 960 with four)
+//   4 bits: one tile up to 16 tokens (16 tokens, E = 64, top-8: 61 us, 68 with two), two up to a
+//     mean of 16 (32 tokens, E = 64: 77 us, 92 with one and 93 with four), then four (128 tokens,
+//     E = 8, top-2, hidden 4096, ffn 14336: 728 us, 785 with two)
+//   bf16: up to 32 tokens one (32, E = 64, top-8: 136 us, 174 with two), from a mean of 4 on two
+//     (24, E = 16, top-4: 79 us, 86 with one); beyond that four, which a skewed router needs (96
+//     tokens, skewed: 92 us, 196 with two; 128 over E = 256: 311 us, 436 with two); from a mean of
+//     16 on eight (128 over E = 8: 737 us, 984 with four)
 static int few_token_tiles(bool mx4, int T, int k, int E) {
   const long long n = (long long)T * k;
   if (T <= 8) return 1;
@@ -1112,7 +1190,7 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   cudaError_t e = cudaSuccess;
   // Up to 8 tokens (one per warp) and bf16 weights the two product kernels route the tokens
   // themselves, in every CTA, instead of waiting for a kernel that does: one launch less (7.9 us of
-  // host time a call, 10.1 with it; one token, E = 128, top-8 takes 14.9 us in all).
+  // host time a call, 10.1 with it; one token, E = 128, top-8 takes 13.9 us in all).
   if (logits && !mx4 && p.T <= 8) {
     p.logits = logits;
     p.top_out = top;

@@ -356,3 +356,34 @@ def test_few_follows_weights_written_just_before():
         run(d, bufs, y)
     for i, y in enumerate(ys):
         assert same(y, ref[i % 2]), i
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("shape", [(16, 256, 128, 1, 1), (30, 256, 128, 8, 1), (9, 384, 128, 5, 3),
+                                   (32, 384, 256, 16, 2), (70, 256, 128, 9, 4),
+                                   (128, 256, 384, 40, 3)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_few_popular_experts(shape, mx4):
+    """Every token names the same first expert, whose entries then make more than one group of
+    columns; every CTA has to make the same groups."""
+    d = make(shape, seed=31, mx4=mx4)
+    d["logits"][:, shape[3] // 2] = 9.0
+    if shape[4] > 2:
+        d["logits"][::2, 0] = 8.0
+    bufs, yg = outputs(d)
+    run(d, bufs, yg[:-1])
+    torch.cuda.synchronize()
+    top, wts = R.route(d["logits"], shape[4])
+    assert int(bufs.status.item()) == 0 and torch.equal(bufs.top_experts.long(), top)
+    assert bool((top[:, 0] == shape[3] // 2).all())
+    y, tol = reference(d, top, bufs.weights.double())
+    R.check(yg[:-1], y, tol, "y")
+    assert (yg[-1] == 7.0).all()
+    # the same routing given, shuffled over the slots of each token
+    order = torch.argsort(torch.rand(top.shape, device="cuda"), 1)
+    bufs2, yg2 = outputs(d)
+    bufs2.top_experts.copy_(top.gather(1, order))
+    bufs2.weights.copy_(bufs.weights.gather(1, order))
+    run(d, bufs2, yg2[:-1], logits=None)
+    torch.cuda.synchronize()
+    R.check(yg2[:-1], y, tol, "y of the given routing")
