@@ -29,9 +29,12 @@
 // 512 columns; instead an epilogue warp takes its 64 columns into registers at once and releases
 // the accumulator before it converts and stores them.
 //
-// Measured at T = 4096, hidden 2048, ffn 1024, E = 64, top-8 (412 GFLOP): GLU 69 us, DOWN 67 us; without
-// the epilogue's work 64 and 59, without MMAs either 60 and 57: what bounds both is the turn of the
-// ring (loads, scale copies, MMAs, release), not the tensor pipe or the stores.
+// Measured at T = 4096, hidden 2048, ffn 1024, E = 64, top-8 (412 GFLOP): GLU 70 us, DOWN 68 us;
+// without the epilogue's work 67 and 61, without MMAs and scale copies as well 54 and 55.  Loads,
+// MMAs and epilogue each come near the whole time, and overlap up to the ring's and the
+// accumulators' hand-overs.  (A second pair of issuing warps for DOWN's second accumulator, each
+// with a ring of its own: 66 us there, 110 instead of 105 at K = 256.  Weights fetched into L2 a
+// tile or more ahead: slower.)
 //
 // Every mbarrier wait is bounded; on expiry the kernel sets DMOE_STATUS_TIMEOUT, raises an
 // abort flag for the other roles of its CTA, drains what it issued and returns.
