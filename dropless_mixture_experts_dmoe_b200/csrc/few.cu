@@ -25,7 +25,7 @@
 // Measured: one token, E = 8, top-2, hidden 4096, ffn 14336 (0.70 GB of bf16 weights) 111 us, 97 % of
 // the copy rate; in counters the first product keeps DRAM 76 % busy and issues on 26 % of the cycles,
 // the second 64 % (its 45 us hold the launch, the routing and the joining of sums).  With 4-bit
-// weights (187 MB) 54 us: the first product is bound by its instructions (34 per 16 x 32 block of
+// weights (187 MB) 53 us: the first product is bound by its instructions (34 per 16 x 32 block of
 // weights: unpacking to fp16 and the scales; 51 % of issue slots, 25 of its 32 us for the loads alone).
 #include "common.cuh"
 #include "kernels.h"

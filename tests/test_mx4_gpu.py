@@ -320,3 +320,39 @@ def test_mx4_forward_stall_reports_timeout_and_context_survives():
     torch.cuda.synchronize()
     assert int(bufs.map.status.item()) == 0
     assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+
+
+@pytest.mark.parametrize("shape", [(5000, 256, 512, 16, 4, 0), (3001, 384, 1152, 40, 6, 0),
+                                   (4100, 128, 128, 100, 3, 0)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_mx4_forward_rows_do_not_depend_on_the_batch(shape):
+    """Many units per pair of SMs, in whole rounds and shares: every token's row is bit for bit what
+    calls over parts of the batch give; the same with two calls in flight on two streams."""
+    dims, x, lg, w, bufs = setup(shape)
+    T, h, f, E, k, flags = shape
+    y = torch.full_like(x, float("nan"))
+    B.dmoe_sparse_map(dims, lg, bufs.map, bufs.ws_map)
+    B.dmoe_mx4_forward(dims, x, *w, bufs.map, y, bufs.ws)
+    step = 700
+    parts = torch.full_like(x, float("nan"))
+    for a in range(0, T, step):
+        n = min(step, T - a)
+        d = B.make_dims(n, h, f, E, k, flags=flags)
+        b = B.Mx4Buffers(d)
+        B.dmoe_sparse_map(d, lg[a:a + n], b.map, b.ws_map)
+        B.dmoe_mx4_forward(d, x[a:a + n], *w, b.map, parts[a:a + n], b.ws)
+    torch.cuda.synchronize()
+    assert int(bufs.map.status.item()) == 0
+    assert torch.isfinite(y.float()).all()
+    assert torch.equal(y.view(torch.int16), parts.view(torch.int16))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [(B.Mx4Buffers(dims), torch.full_like(x, float("nan"))) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (b, out) in zip(streams, both):
+            B.dmoe_sparse_map(dims, lg, b.map, b.ws_map, stream=s)
+            B.dmoe_mx4_forward(dims, x, *w, b.map, out, b.ws, stream=s)
+    torch.cuda.synchronize()
+    for b, out in both:
+        assert int(b.map.status.item()) == 0
+        assert torch.equal(y.view(torch.int16), out.view(torch.int16))
