@@ -157,10 +157,10 @@ def version() -> str:
     return load().dmoe_version().decode()
 
 
-def dmoe_debug_inject_stall(enable: bool = True) -> None:
-    """Test-only: the next grouped-GEMM launch stalls on purpose and reports
-    STATUS_TIMEOUT (see include/dmoe.h)."""
-    _check(load().dmoe_debug_inject_stall(1 if enable else 0), "dmoe_debug_inject_stall")
+def dmoe_debug_inject_stall(nth: int = 1) -> None:
+    """Test-only: the nth grouped-GEMM launch from now (True: the next; 0: none) stalls on purpose
+    and reports STATUS_TIMEOUT (see include/dmoe.h)."""
+    _check(load().dmoe_debug_inject_stall(int(nth)), "dmoe_debug_inject_stall")
 
 
 def make_dims(T: int, hidden: int, ffn: int, num_experts: int, top_k: int,

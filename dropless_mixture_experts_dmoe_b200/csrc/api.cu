@@ -844,8 +844,8 @@ const char *dmoe_status_string(int32_t status) {
 
 const char *dmoe_version(void) { return "dmoe-b200 0.1"; }
 
-int dmoe_debug_inject_stall(int enable) {
-  set_inject_stall(enable);
+int dmoe_debug_inject_stall(int nth) {
+  set_inject_stall(nth);
   return DMOE_OK;
 }
 

@@ -1156,11 +1156,16 @@ static int raster_units(int K) {
   return (int)g;
 }
 
-// Test-only stall injection (dmoe_debug_inject_stall): consumed by the next GEMM launch.
+// Test-only stall injection (dmoe_debug_inject_stall): the launches until the one that stalls.
 static std::atomic<int> g_inject_stall{0};
 
-void set_inject_stall(int on) { g_inject_stall.store(on ? 1 : 0); }
-int take_inject_stall() { return g_inject_stall.exchange(0); }
+void set_inject_stall(int nth) { g_inject_stall.store(nth > 0 ? nth : 0); }
+int take_inject_stall() {
+  int n = g_inject_stall.load();
+  while (n > 0 && !g_inject_stall.compare_exchange_weak(n, n - 1)) {
+  }
+  return n == 1;
+}
 
 template <int MODE, int EPI>
 static cudaError_t launch_gemm(const GemmParams &p_in, long long max_tiles, cudaStream_t st) {

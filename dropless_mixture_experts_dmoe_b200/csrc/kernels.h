@@ -215,8 +215,9 @@ cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs
 
 int device_sm_count();
 
-// Test-only: make the next grouped-GEMM launch stall on purpose (see dmoe_debug_inject_stall).
-void set_inject_stall(int on);
-int take_inject_stall();  // what is set, cleared
+// Test-only: make the nth grouped-GEMM launch from now stall on purpose (see
+// dmoe_debug_inject_stall).
+void set_inject_stall(int nth);
+int take_inject_stall();  // counts a launch; 1 if it is the one
 
 }  // namespace dmoe

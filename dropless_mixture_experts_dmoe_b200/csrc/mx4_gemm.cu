@@ -489,6 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     };
     uint32_t acc_phase = 0;
     int t = mine_acc;
+    int good = 1;  // 0 once a wait of this warp expired
     MxTile nx;
     float wnx = 0.0f;
     if (t < count) {
@@ -499,10 +500,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       const MxTile tl = nx;
       const float wr = wnx;
       const int row = tl.row0 + sub * 32 + lane;
-      int good = 1;
-      if (lane == 0)
+      if (lane == 0 && good)
         good = mbar_wait(&tfull[mine_acc], acc_phase, p.status, abort_flag, p.wait_cycles) ? 1 : 0;
-      if (!__shfl_sync(0xFFFFFFFFu, good, 0)) break;
+      good = __shfl_sync(0xFFFFFFFFu, good, 0);
+      // DOWN: one warp of a pair may see the abort flag where the other's wait still passed, so a
+      // warp goes on to the pair's next barrier, says so there, and both leave at the same tile
+      if (GLU && !good) break;
       acc_phase ^= 1u;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(mine_acc * C::N);
@@ -514,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0)  // accumulator free: values in registers
+      if (lane == 0 && good)  // accumulator free: values in registers
         mbar_arrive_remote(leader_tempty0 + (uint32_t)(mine_acc * sizeof(uint64_t)));
       t += C::nacc;
       if (t < count) {
@@ -530,6 +533,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         uint32_t mb = 0u;  // largest magnitude, as integers (NaN above inf)
 #pragma unroll
         for (int i = 0; i < 32; ++i) mb = max(mb, max(v0[i] & 0x7FFFFFFFu, v1[i] & 0x7FFFFFFFu));
+        constexpr uint32_t kExpired = 0xFFFFFFFFu;  // above every magnitude
+        if (!good) mb = kExpired;
         // ... of the 128-column group: exchanged with the warp of its other 64 columns
         uint32_t *mine = reinterpret_cast<uint32_t *>(amax) + (warp - 2) * 32 + lane;
         uint32_t *other = mine + (part ? -128 : 128);  // four warps on
@@ -538,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
         asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
         mb = max(mb, *other);
         asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // read before the next tile's
+        if (mb == kExpired) break;  // in every lane of both warps
         float stored;
         const float k = bfp_scale(__uint_as_float(mb) * fabsf(wr), stored) * wr;
         if (part == 0) p.yscale[(size_t)row * dmoe_scale_stride(p.h) + n0 / 128] = stored;
