@@ -158,8 +158,8 @@ def version() -> str:
 
 
 def dmoe_debug_inject_stall(nth: int = 1) -> None:
-    """Test-only: the nth grouped-GEMM launch from now (True: the next; 0: none) stalls on purpose
-    and reports STATUS_TIMEOUT (see include/dmoe.h)."""
+    """Test-only: the nth product-kernel launch from now (True: the next; 0: none) stalls on
+    purpose and reports STATUS_TIMEOUT (see include/dmoe.h)."""
     _check(load().dmoe_debug_inject_stall(int(nth)), "dmoe_debug_inject_stall")
 
 

@@ -628,24 +628,31 @@ struct FewKernel {
 
   // pre: the weights of the first stages are loaded before the wait for the earlier kernels.
   __device__ __forceinline__ void produce(int item0, bool pre, int loader, int lane) const {
-    FewPos q = first(item0), w = q;
+    FewPos q = first(item0);
+    int st = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    if (p.inject && q.on) {  // test-only: the first stage is withheld, and the waits for it expire
+      next(q);
+      st = 1;
+      issued = 1;
+    }
     if (pre) {
-      for (int st = 0; st < C::P && w.on; ++st) {
+      FewPos w = q;
+      for (int i = st; i < C::P && w.on; ++i) {
         if (loader == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&full[st], bytes(w));
-          load_w(w, st);
+          mbar_arrive_expect_tx(&full[i], bytes(w));
+          load_w(w, i);
         }
         next(w);
       }
       pdl_wait();
     }
-    int st = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
     while (q.on) {
       if (issued >= C::P) {
         int good = 1;
-        if (lane == 0) good = mbar_wait(&empty[st], phase ^ 1u, p.status, abort_flag) ? 1 : 0;
+        if (lane == 0)
+          good = mbar_wait(&empty[st], phase ^ 1u, p.status, abort_flag, p.wait_cycles) ? 1 : 0;
         if (!__shfl_sync(0xFFFFFFFFu, good, 0)) break;
       }
       if (loader == 0 && lane == 0 && !(pre && issued < C::P)) {
@@ -663,7 +670,7 @@ struct FewKernel {
     }
     if (lane == 0)  // every copy has landed before the CTA's memory is given up
       for (long long i = (issued > C::P ? issued - C::P : 0); i < issued; ++i)
-        mbar_wait_plain(&full[i % C::P], (uint32_t)((i / C::P) & 1));
+        mbar_wait_plain(&full[i % C::P], (uint32_t)((i / C::P) & 1), p.wait_cycles);
   }
 
   // ---- the multiplying warps ----
@@ -827,13 +834,19 @@ struct FewKernel {
     for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     int st = 0;
     uint32_t phase = 0;
+    bool good = true;  // until a wait expires
     int tile0 = 0;
     for (FewPos q = first(item0); q.on; next(q)) {
       if (C::MX4 && q.chunk == q.c0) tile0 = (tile_of(q) * C::outs) & 127;
-      if (!mbar_wait(&full[st], phase, p.status, abort_flag)) *abort_flag = 1;
+      if (!mbar_wait(&full[st], phase, p.status, abort_flag, p.wait_cycles)) {
+        *abort_flag = 1;
+        good = false;
+      }
       multiply(q, tile0, st, r, s, lane, zero, acc);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      // a stage that was not waited for to the end, and those behind it, are not given back: their
+      // copies may be under way, and the loading warps then stop at the abort flag
+      if (lane == 0 && good) mbar_arrive(&empty[st]);
       if (++st == C::P) {
         st = 0;
         phase ^= 1u;
@@ -1052,6 +1065,12 @@ int few_places(size_t smem) {
   return device_sm_count() * (n < 1 ? 1 : n < C::min_ctas ? n : C::min_ctas);
 }
 
+// Limit of the kernel's waits, and whether its first stage is withheld.
+void few_limits(FewParams &p) {
+  p.inject = take_inject_stall();
+  p.wait_cycles = p.inject ? kInjectedWaitCycles : kWaitCycles;
+}
+
 template <class C>
 cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
@@ -1060,6 +1079,7 @@ cudaError_t launch_few_glu(FewParams p, cudaStream_t st) {
   const long long ef = (long long)p.E * p.f;
   if (!few_map<C>(&p.tw[0], p.w1.data, ef, p.h) || !few_map<C>(&p.tw[1], p.w3.data, ef, p.h))
     return cudaErrorInvalidValue;
+  few_limits(p);
   p.ws[0] = static_cast<const uint8_t *>(p.w1.scales);
   p.ws[1] = static_cast<const uint8_t *>(p.w3.scales);
   const size_t smem = C::fixed + few_list_bytes(p);
@@ -1075,6 +1095,7 @@ cudaError_t launch_few_down(FewParams p, cudaStream_t st) {
   cudaError_t e = allow_smem(k_few_down<C>, done, kFewSmem);
   if (e != cudaSuccess) return e;
   if (!few_map<C>(&p.tw[0], p.w2.data, (long long)p.E * p.h, p.f)) return cudaErrorInvalidValue;
+  few_limits(p);
   p.tw[1] = p.tw[0];
   p.ws[0] = p.ws[1] = static_cast<const uint8_t *>(p.w2.scales);
   const size_t smem = C::fixed + few_list_bytes(p) +

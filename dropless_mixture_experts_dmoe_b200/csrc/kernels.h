@@ -184,6 +184,8 @@ struct FewParams {
   CUtensorMap tw[2];  // W1 and W3, or W2
   const uint8_t *ws[2];
   int32_t *status;
+  int inject;  // test-only: the first stage of every CTA is withheld (waits then expire)
+  long long wait_cycles;
   // set where the product kernels route the tokens themselves
   const uint16_t *logits;
   bool renorm;
@@ -215,7 +217,7 @@ cudaError_t launch_mx4_down(const GemmProblem &g, const void *hq, const void *hs
 
 int device_sm_count();
 
-// Test-only: make the nth grouped-GEMM launch from now stall on purpose (see
+// Test-only: make the nth launch of a product kernel from now stall on purpose (see
 // dmoe_debug_inject_stall).
 void set_inject_stall(int nth);
 int take_inject_stall();  // counts a launch; 1 if it is the one
