@@ -225,6 +225,7 @@ class SparseMap:
             raise DMoEError(-2, "SparseMap")
         i32 = dict(dtype=torch.int32, device=device)
         self.dims = dims
+        self._kind = _map_kind(dims)  # dims is the caller's object, which may change
         rounding = bool(dims.flags & ROUTE_TOKEN_ROUNDING)
         N = dmoe_entries_max(dims)
         if rounding:  # experts and weights of the token-major entry list
@@ -502,6 +503,11 @@ def _sizes(dims) -> tuple:
     return dims.T, dims.hidden, dims.ffn, dims.num_experts, dims.top_k
 
 
+def _map_kind(dims) -> tuple:
+    """What a map is made for: the sizes, and whether it is token rounding's entry list."""
+    return (*_sizes(dims), bool(dims.flags & ROUTE_TOKEN_ROUNDING))
+
+
 def _few_args(dims, x, logits, bufs, y, dev):
     if bufs._sizes != _sizes(dims):
         raise ValueError(f"the buffers are those of sizes {bufs._sizes}, not of {_sizes(dims)}")
@@ -563,8 +569,9 @@ def dmoe_mx4_forward(dims: dmoe_dims, x, w1: Mx4, w3: Mx4, w2: Mx4, smap: Sparse
     """y [T,h] = the layer with every product in the microscaled 4-bit format (inference)."""
     E, h, f, row = dims.num_experts, dims.hidden, dims.ffn, (dims.T, dims.hidden)
     dev = _device()
-    if _sizes(smap.dims) != _sizes(dims):
-        raise ValueError(f"the map is that of {smap.dims}, not of {dims}")
+    if smap._kind != _map_kind(dims):
+        raise ValueError("the map is that of (T, hidden, ffn, num_experts, top_k, token rounding) = "
+                         f"{smap._kind}, not of {_map_kind(dims)}")
     _arg("smap.status", smap.status, (1,), torch.int32, dev)
     _check(load().dmoe_mx4_forward(ctypes.byref(dims), _arg("x", x, row, torch.bfloat16, dev),
                                    w1.arg("w1", (E, f, h), dev), w3.arg("w3", (E, f, h), dev),
