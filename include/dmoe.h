@@ -478,7 +478,8 @@ typedef struct {
 
 /* src [rows, cols] bf16 -> dst.  Per block, with m the largest magnitude,
  * s = floor(log2 m) - 2 + 127 kept within [0, 254] (0 for an all-zero block) and every element
- * the nearest e2m1 value to x / 2^(s - 127), ties to the even mantissa, saturated at +-6.  A
+ * the nearest e2m1 value to x / 2^(s - 127), ties to the even mantissa, saturated at +-6, with
+ * the sign bit of x (-0.0 and negative values that round to zero are element 8, -0).  A
  * block that holds an inf or NaN gets the scale NaN and zero codes.  Scale bytes of the rows
  * that fill the last tile are written as 0. rows >= 1.  DMOE_ERR_SHAPE for
  * rows < 1 or cols not a multiple of 128, DMOE_ERR_TOO_LARGE past 2^40 rows or 2^23 columns. */
