@@ -37,6 +37,7 @@ namespace dmoe {
 namespace {
 
 constexpr int kRouteWarps = 8;
+constexpr float kMaxBf16 = 0x1.FEp127f;
 constexpr int kFewSmem = 226 * 1024;  // dynamic shared memory of a CTA at most
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -946,11 +947,11 @@ __global__ void __launch_bounds__(C::threads, C::min_ctas)
           } else {
             const float hv = silu_f(v[c]) * v[2 + c];
             const size_t at = (size_t)(en & 0xFFFFu) * p.f + q.b * C::outs + col;
-            const __nv_bfloat16 hi = __float2bfloat16(hv);
-            const float rest = hv - __bfloat162float(hi);
+            // the upper part stops at bf16's largest value: up to fp32's the lower part holds the
+            // rest, and of an inf or NaN the lower part is one
+            const __nv_bfloat16 hi = __float2bfloat16(fminf(fmaxf(hv, -kMaxBf16), kMaxBf16));
             p.hout[at] = __bfloat16_as_ushort(hi);
-            // inf - inf: the upper part already says it
-            p.hlo[at] = __bfloat16_as_ushort(__float2bfloat16(rest == rest ? rest : 0.0f));
+            p.hlo[at] = __bfloat16_as_ushort(__float2bfloat16(hv - __bfloat162float(hi)));
           }
         }
       },
