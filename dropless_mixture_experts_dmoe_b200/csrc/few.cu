@@ -568,7 +568,7 @@ struct FewKernel {
   }
   __device__ __forceinline__ uint32_t bytes(const FewPos &q) const {  // that bulk copies bring
     const uint32_t w = width(q), nr = min(q.cnt, 8 * C::NT);
-    return C::w_bytes + (C::MX4 ? C::mats * (w >> 7) * kMx4TileBytes : 0) +
+    return p.withheld + C::w_bytes + (C::MX4 ? C::mats * (w >> 7) * kMx4TileBytes : 0) +
            (C::xbulk ? nr * (C::BR * w * 2 + (C::SB ? w >> 3 : 0)) : 0);
   }
   // Weights and their scales (one lane).
@@ -629,26 +629,20 @@ struct FewKernel {
 
   // pre: the weights of the first stages are loaded before the wait for the earlier kernels.
   __device__ __forceinline__ void produce(int item0, bool pre, int loader, int lane) const {
-    FewPos q = first(item0);
-    int st = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    if (p.inject && q.on) {  // test-only: the first stage is withheld, and the waits for it expire
-      next(q);
-      st = 1;
-      issued = 1;
-    }
+    FewPos q = first(item0), w = q;
     if (pre) {
-      FewPos w = q;
-      for (int i = st; i < C::P && w.on; ++i) {
+      for (int st = 0; st < C::P && w.on; ++st) {
         if (loader == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&full[i], bytes(w));
-          load_w(w, i);
+          mbar_arrive_expect_tx(&full[st], bytes(w));
+          load_w(w, st);
         }
         next(w);
       }
       pdl_wait();
     }
+    int st = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
     while (q.on) {
       if (issued >= C::P) {
         int good = 1;
@@ -1066,10 +1060,11 @@ int few_places(size_t smem) {
   return device_sm_count() * (n < 1 ? 1 : n < C::min_ctas ? n : C::min_ctas);
 }
 
-// Limit of the kernel's waits, and whether its first stage is withheld.
+// Limit of the kernel's waits, and what its stages wait for in vain.
 void few_limits(FewParams &p) {
-  p.inject = take_inject_stall();
-  p.wait_cycles = p.inject ? kInjectedWaitCycles : kWaitCycles;
+  const int inject = take_inject_stall();
+  p.withheld = inject ? 16u : 0u;
+  p.wait_cycles = inject ? kInjectedWaitCycles : kWaitCycles;
 }
 
 template <class C>

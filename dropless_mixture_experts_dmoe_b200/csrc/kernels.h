@@ -184,7 +184,7 @@ struct FewParams {
   CUtensorMap tw[2];  // W1 and W3, or W2
   const uint8_t *ws[2];
   int32_t *status;
-  int inject;  // test-only: the first stage of every CTA is withheld (waits then expire)
+  uint32_t withheld;  // test-only: bytes that every stage expects and never gets (waits expire)
   long long wait_cycles;
   // set where the product kernels route the tokens themselves
   const uint16_t *logits;

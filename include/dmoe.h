@@ -519,9 +519,9 @@ DMOE_API const char *dmoe_version(void);
 /* Test-only fault injection (no counterpart on the pages; it exercises the library's own
  * failure path).  The nth launch of a product kernel of this process from now (nth = 1: the
  * next; any grouped GEMM, the 4-bit ones too, and the two products of the few-token calls) runs
- * with a wait budget of ~10^7 cycles, and its pair leaders (few tokens: every CTA) withhold
- * their first operand stage: the bounded wait on that stage expires, the kernel sets
- * DMOE_STATUS_TIMEOUT in the call's status word, every role of every CTA leaves through its own
+ * with a wait budget of ~10^7 cycles, and its pair leaders withhold their first operand stage
+ * (few tokens: every stage expects more than it gets): the bounded wait on it expires, the
+ * kernel sets DMOE_STATUS_TIMEOUT in the call's status word, every role of every CTA leaves through its own
  * bounded waits, and the launch returns normally with that launch's results invalid.  No
  * trap, no fault; the context stays usable.  The switch clears itself on that launch; nth <= 0
  * clears it at once. */

@@ -1,5 +1,5 @@
-"""Expired waits of the serving kernels, without a fault: the first operand stage of one launch is
-withheld on purpose; the launch must report the timeout, return, and leave the context usable."""
+"""Expired waits of the serving kernels, without a fault: operands of one launch are withheld on
+purpose; the launch must report the timeout, return, and leave the context usable."""
 import time
 
 import pytest
