@@ -37,6 +37,7 @@ namespace dmoe {
 namespace {
 
 constexpr int kRouteWarps = 8;
+constexpr int kRouteRegs = 8;  // experts per lane of a routing warp in registers
 constexpr float kMaxBf16 = 0x1.FEp127f;
 constexpr int kFewSmem = 226 * 1024;  // dynamic shared memory of a CTA at most
 
@@ -69,7 +70,7 @@ __device__ __forceinline__ void route_token(const uint16_t *__restrict__ row, in
                                             bool &bad) {
   auto image = [&](int e) -> uint32_t { return (uint32_t)__ldcg(row + e) << 16; };
   auto key_of = [&](uint32_t im, int e) { return route_key_nan(im, 0xFFFFu - (uint32_t)e); };
-  constexpr int R = 8;  // experts per lane in registers
+  constexpr int R = kRouteRegs;
   uint32_t im[R], key[R];
   bad = false;
 #pragma unroll
@@ -1207,8 +1208,11 @@ cudaError_t launch_few(const FewParams &p_in, const uint16_t *logits, bool renor
   cudaError_t e = cudaSuccess;
   // Up to 8 tokens (one per warp) and bf16 weights the two product kernels route the tokens
   // themselves, in every CTA, instead of waiting for a kernel that does: one launch less (7.9 us of
-  // host time a call, 10.1 with it; one token, E = 128, top-8 takes 13.9 us in all).
-  if (logits && !mx4 && p.T <= 8) {
+  // host time a call, 10.1 with it; one token, E = 128, top-8 takes 13.7 us in all).  With more
+  // experts than a warp keeps in registers each CTA would read the logits again for every pick
+  // (hidden 1536, ffn 256, top-8: one token at E = 1024 42.8 us, 27.2 with the kernel; at E = 512
+  // 24.5 and 18.0; with top-2 12.0 and 14.2).
+  if (logits && !mx4 && p.T <= 8 && p.E <= kRouteRegs * 32) {
     p.logits = logits;
     p.top_out = top;
     p.weights_out = weights;
