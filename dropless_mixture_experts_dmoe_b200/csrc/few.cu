@@ -373,7 +373,7 @@ __device__ __forceinline__ void few_put(const FewParams &p, const FewLists &l, i
 }
 
 // The lists of up to 32 entries, by one warp: places by counting smaller keys (expert, entry).
-// One token, E = 128, top-8: 13.9 us, 16.4 with the lists for any number.
+// One token, E = 128, top-8: 13.7 us, 16.4 with the lists for any number.
 template <class C>
 __device__ __forceinline__ int few_lists32(const FewParams &p, const FewLists &l, int lane) {
   const int n = p.T * p.k;
@@ -511,7 +511,7 @@ __device__ __forceinline__ int few_lists(const FewParams &p, const FewLists &l, 
 
 // A place in a CTA's stream of stages: item (GLU: group, row tile; DOWN: group, part of K), chunk
 // of K.  Groups of one expert are items of their own, which different CTAs take: with a CTA
-// that went through all groups of its expert, 96 tokens on a skewed router took 105 us, now 95.
+// that went through all groups of its expert, 96 tokens on a skewed router took 105 us, now 92.
 struct FewPos {
   int a, b;             // group; tile or part
   int e, n0, cnt;       // expert, first entry, entries (8 NT at most, which its users say again:

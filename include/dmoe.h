@@ -452,8 +452,9 @@ DMOE_API int dmoe_router_backward(const dmoe_dims *dims, const void *x, const vo
  * Needs no map.  DMOE_ROUTE_RENORMALIZE is followed; DMOE_SAVE_X_ONLY and DMOE_FUSED_COMBINE
  * choose between forms of dmoe_forward and change nothing here; DMOE_ROUTE_TOKEN_ROUNDING and
  * T > DMOE_FEW_MAX_TOKENS are DMOE_ERR_SHAPE.  x and y may be the same rows.  Results are
- * deterministic.  From about 16 tokens per expert on, dmoe_sparse_map + dmoe_forward (whole
- * 128-row blocks on the tensor cores) take less time. */
+ * deterministic.  H is held in 16 bits (as two bf16).  From a mean of about 8 tokens per expert
+ * (hidden 4096, ffn 14336) to 16 (hidden 2048, ffn 1024) on, dmoe_sparse_map + dmoe_forward
+ * (whole 128-row blocks on the tensor cores) take less time. */
 DMOE_API int dmoe_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
                               const void *w1, const void *w3, const void *w2,
                               int32_t *top_experts, float *weights, void *y, int32_t *status,
@@ -490,10 +491,15 @@ DMOE_API int dmoe_mx4_quantize(int64_t rows, int64_t cols, const void *src, cons
 DMOE_API int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src, void *dst,
                                  void *stream);
 
-/* dmoe_forward_few over expert weights in the format (w1, w3 as [E * f, h], w2 as [E * h, f]);
- * x and the sums keep their precision, only the weights have four bits.  A row of x is scaled by a
- * power of two that takes its largest value to 2^15, so weights beyond 2^100 can overflow the
- * fp32 sums where the true result does not. */
+/* dmoe_forward_few over expert weights in the format (w1, w3 as [E * f, h], w2 as [E * h, f]).
+ * x and H are not converted to four bits, but held in fp16 under powers of two that take the
+ * largest value of a row of x, or of 32 columns of H, to between 2^14 and 2^15: x is exact down to
+ * 2^-29 of its row's largest value (below that off by at most 2^-39 of it; the powers of two stop
+ * at 2^126, so rows below 2^-112 keep less), H has 11 bits.  Sums are fp32; under these scales weights beyond 2^100, or values of H beyond 2^119, can overflow
+ * them where the true result does not.
+ * From a mean of about 4 to 8 tokens per expert on, dmoe_sparse_map + dmoe_mx4_forward take less
+ * time (hidden 4096, ffn 14336, E = 8, top-2: 32 tokens 220 us against 253, 128 tokens 214
+ * against 740), but convert x and H to four bits too. */
 DMOE_API int dmoe_mx4_forward_few(const dmoe_dims *dims, const void *x, const void *logits,
                                   const dmoe_mx4 *w1, const dmoe_mx4 *w3, const dmoe_mx4 *w2,
                                   int32_t *top_experts, float *weights, void *y,
@@ -502,7 +508,9 @@ DMOE_API int dmoe_mx4_forward_few(const dmoe_dims *dims, const void *x, const vo
 /* The layer for many tokens with both operands of every product in the format (inference):
  * token rows of x are converted as dmoe_mx4_quantize does, H = silu(A) * Bm is converted from
  * fp32 in the same way, and the products run on the block-scaled tensor cores with fp32
- * accumulation.  map: from dmoe_sparse_map.  y [T,h] bf16, the weighted sum of a token's rows.
+ * accumulation.  map: from dmoe_sparse_map, for the same sizes and the same choice of
+ * DMOE_ROUTE_TOKEN_ROUNDING.  y [T,h] bf16, the weighted sum of a token's rows, which are held in
+ * fp16 under a power of two per 128 columns (as in dmoe_forward).
  * ws: dmoe_workspace_bytes(dims, DMOE_WS_MX4_FORWARD) bytes.  DMOE_SAVE_X_ONLY and
  * DMOE_FUSED_COMBINE change nothing here; both routing flags are followed through the map. */
 DMOE_API int dmoe_mx4_forward(const dmoe_dims *dims, const void *x, const dmoe_mx4 *w1,
