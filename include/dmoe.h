@@ -495,8 +495,9 @@ DMOE_API int dmoe_mx4_dequantize(int64_t rows, int64_t cols, const dmoe_mx4 *src
  * x and H are not converted to four bits, but held in fp16 under powers of two that take the
  * largest value of a row of x, or of 32 columns of H, to between 2^14 and 2^15: x is exact down to
  * 2^-29 of its row's largest value (below that off by at most 2^-39 of it; the powers of two stop
- * at 2^126, so rows below 2^-112 keep less), H has 11 bits.  Sums are fp32; under these scales weights beyond 2^100, or values of H beyond 2^119, can overflow
- * them where the true result does not.
+ * at 2^126, so rows below 2^-112 keep less), H has 11 bits.  Sums are fp32; under these scales
+ * weights beyond 2^100, or values of H beyond 2^119, can overflow them where the true result does
+ * not.
  * From a mean of about 4 to 8 tokens per expert on, dmoe_sparse_map + dmoe_mx4_forward take less
  * time (hidden 4096, ffn 14336, E = 8, top-2: 32 tokens 220 us against 253, 128 tokens 214
  * against 740), but convert x and H to four bits too. */
